@@ -51,6 +51,13 @@ SIGNATURES = {
                                      _i32, _i32, _i32, _f32, _vp, _vp, _vp, _sz, _vp, _vp]),
     "sa_sparse_attn_decode_noalloc": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _i32,
                                              _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _vp]),
+    "sa_cache_append": (_i32, [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32,
+                               _i32, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _vp]),
+    "sa_cache_append_q8": (_i32, [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32,
+                                  _i32, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _i32,
+                                  _vp, _vp]),
+    "sa_sparse_attn_q8": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _i32, _i32,
+                                 _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _vp]),
     "sa_pool_index_keys": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp]),
     "sa_coarse_block_counts": (_i32, [_i32, _i32, _i32, _vp, _vp]),
     "sa_expand_blocks": (_i32, [_vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp]),
@@ -194,6 +201,117 @@ def sa_sparse_attn_decode_noalloc(q, k_cache, v_cache, page_table, max_pages, po
 
 
 SA_DECODE_NOALLOC_SCRATCH_BYTES = 16 << 20
+
+
+def _on_device(where, tensors, rows=()):
+    """The one GPU that all tensors of a call are on.  tensors: (name, tensor or
+    None, dtypes, least number of elements), contiguous; rows: the same for
+    tensors of rows with a stride of their own (name, tensor, dtypes, rows, row
+    length, stride)."""
+    dev = -1
+    for name, t, dtypes, numel in tensors:
+        if t is None:
+            continue
+        at = t.get_device()
+        if at < 0 or (dev >= 0 and at != dev):
+            raise ValueError("%s: %s is not on the GPU of the other tensors" % (where, name))
+        dev = at
+        if t.dtype not in dtypes or not t.is_contiguous() or t.numel() < numel:
+            raise ValueError("%s: %s must be a contiguous %s tensor of at least %d elements"
+                             % (where, name, " or ".join(map(str, dtypes)), numel))
+    for name, t, dtypes, n, width, ld in rows:
+        if t is None:
+            continue
+        if t.get_device() != dev:
+            raise ValueError("%s: %s is not on the GPU of the other tensors" % (where, name))
+        if t.dtype not in dtypes:
+            raise ValueError("%s: %s must be a %s tensor" % (where, name, " or ".join(map(str, dtypes))))
+        if t.is_contiguous():
+            short = t.numel() < (n - 1) * ld + width
+        else:   # a slice of wider rows: [rows, width or more], ld apart
+            short = (t.dim() != 2 or t.shape[0] < n or t.shape[1] < width or t.stride(1) != 1 or t.stride(0) != ld)
+        if n > 0 and short:
+            raise ValueError("%s: %s does not hold %d rows of %d elements, %d apart" % (where, name, n, width, ld))
+    return dev
+
+
+def _call(where, dev, stream, *args):
+    """The C call `where` on the tensors' GPU, on `stream` or that GPU's current stream."""
+    import torch
+    raw = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+    fn = getattr(_lib, where)
+    if dev == torch.cuda.current_device():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    _check(status, where)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _append_args(where, q, ld_q, q_out, k, ld_k, v, ld_v, kI, ld_kI, n_valid, page_table, max_pages, pool_pages, S_max, B,
+                 T, Hq, d, D_I, inv_freq, rot_dim, k_cache, v_cache, kI_cache, kI_e4m3, dev_status, cache_dtypes, more=()):
+    import torch
+    bf, i32 = (torch.bfloat16,), (torch.int32,)
+    R, n = B * T, pool_pages * 64 if page_table is not None else B * S_max
+    byte = (torch.uint8, torch.float8_e4m3fn)
+    return _on_device(where, (
+        ("k_cache", k_cache, cache_dtypes, n * d), ("v_cache", v_cache, cache_dtypes, n * d),
+        ("n_valid", n_valid, i32, R), ("page_table", page_table, i32, B * max_pages),
+        ("q_out", q_out, bf, R * Hq * d), ("inv_freq", inv_freq, (torch.float32,), rot_dim // 2),
+        ("kI_cache", kI_cache, byte if kI_e4m3 else bf, n * D_I), ("dev_status", dev_status, i32, 1)) + more,
+        (("q", q, bf, R, Hq * d, ld_q), ("k", k, bf, R, d, ld_k), ("v", v, bf, R, d, ld_v), ("kI", kI, bf, R, D_I, ld_kI)))
+
+
+def sa_cache_append(q, ld_q, q_out, k, ld_k, v, ld_v, kI, ld_kI, n_valid, page_table, max_pages, pool_pages, page_size,
+                    S_max, B, T, Hq, d, D_I, inv_freq, rot_dim, interleaved, k_cache, v_cache, kI_cache, kI_e4m3,
+                    dev_status=None, stream=None):
+    """Append the rotated keys and the values of new tokens to a bf16 cache (and
+    the index keys to theirs), and rotate the queries.  q, k, v and kI may be
+    slices of wider rows (ld_* elements apart)."""
+    import torch
+    dev = _append_args("sa_cache_append", q, ld_q, q_out, k, ld_k, v, ld_v, kI, ld_kI, n_valid, page_table, max_pages,
+                       pool_pages, S_max, B, T, Hq, d, D_I, inv_freq, rot_dim, k_cache, v_cache, kI_cache, kI_e4m3,
+                       dev_status, (torch.bfloat16,))
+    _call("sa_cache_append", dev, stream, _addr(q), ld_q, _addr(q_out), _addr(k), ld_k, _addr(v), ld_v, _addr(kI), ld_kI,
+          _addr(n_valid), _addr(page_table), max_pages, pool_pages, page_size, S_max, B, T, Hq, d, D_I, _addr(inv_freq),
+          rot_dim, interleaved, _addr(k_cache), _addr(v_cache), _addr(kI_cache), kI_e4m3, _addr(dev_status))
+
+
+def sa_cache_append_q8(q, ld_q, q_out, k, ld_k, v, ld_v, kI, ld_kI, n_valid, page_table, max_pages, pool_pages, page_size,
+                       S_max, B, T, Hq, d, D_I, inv_freq, rot_dim, interleaved, k_cache, v_cache, k_scale, v_scale,
+                       scale_block, kI_cache, kI_e4m3, dev_status=None, stream=None):
+    """The same append into an 8-bit cache (uint8 or float8_e4m3fn tensors) with a scale for each scale_block tokens."""
+    import torch
+    n = (pool_pages * 64 if page_table is not None else B * S_max) // max(scale_block, 1)
+    f32, f8 = (torch.float32,), (torch.uint8, torch.float8_e4m3fn)
+    dev = _append_args("sa_cache_append_q8", q, ld_q, q_out, k, ld_k, v, ld_v, kI, ld_kI, n_valid, page_table, max_pages,
+                       pool_pages, S_max, B, T, Hq, d, D_I, inv_freq, rot_dim, k_cache, v_cache, kI_cache, kI_e4m3,
+                       dev_status, f8, (("k_scale", k_scale, f32, n), ("v_scale", v_scale, f32, n)))
+    _call("sa_cache_append_q8", dev, stream, _addr(q), ld_q, _addr(q_out), _addr(k), ld_k, _addr(v), ld_v, _addr(kI),
+          ld_kI, _addr(n_valid), _addr(page_table), max_pages, pool_pages, page_size, S_max, B, T, Hq, d, D_I,
+          _addr(inv_freq), rot_dim, interleaved, _addr(k_cache), _addr(v_cache), _addr(k_scale), _addr(v_scale),
+          scale_block, _addr(kI_cache), kI_e4m3, _addr(dev_status))
+
+
+def sa_sparse_attn_q8(q, k_cache, v_cache, k_scale, v_scale, scale_block, page_table, max_pages, pool_pages, page_size,
+                      S_max, n_valid, topk, K, W, B, T, Hq, d, scale, out, lse=None, dev_status=None, stream=None):
+    """Selected-key attention over an 8-bit cache, T rows a sequence."""
+    import torch
+    R, n = B * T, pool_pages * 64 if page_table is not None else B * S_max
+    i32, f32, bf = (torch.int32,), (torch.float32,), (torch.bfloat16,)
+    f8, ns = (torch.uint8, torch.float8_e4m3fn), n // max(scale_block, 1)
+    dev = _on_device("sa_sparse_attn_q8", (
+        ("q", q, bf, R * Hq * d), ("k_cache", k_cache, f8, n * d), ("v_cache", v_cache, f8, n * d),
+        ("k_scale", k_scale, f32, ns), ("v_scale", v_scale, f32, ns), ("page_table", page_table, i32, B * max_pages),
+        ("n_valid", n_valid, i32, R), ("topk", topk, i32, R * K), ("out", out, bf, R * Hq * d), ("lse", lse, f32, R * Hq),
+        ("dev_status", dev_status, i32, 1)))
+    _call("sa_sparse_attn_q8", dev, stream, _addr(q), _addr(k_cache), _addr(v_cache), _addr(k_scale), _addr(v_scale),
+          scale_block, _addr(page_table), max_pages, pool_pages, page_size, S_max, _addr(n_valid), _addr(topk), K, W, B, T,
+          Hq, d, scale, _addr(out), _addr(lse), _addr(dev_status))
 
 
 def sa_pool_index_keys(kI, S, D_I, block, kB, stream=None):

@@ -1,0 +1,418 @@
+// cache_append.cu -- fill the caches that the indexer, the top-K and the
+// attention read: rotate new keys (and queries) to their positions, round or
+// quantise them, and store them in their slots.
+//
+//   x'_first  = x_first cos a_i - x_second sin a_i,   a_i = p * inv_freq[i]
+//   x'_second = x_second cos a_i + x_first sin a_i
+//
+// The angle p * inv_freq[i] is an exact fp64 product (a position below 2^31
+// times 24 bits); its turn count's fraction is taken in fp64 and only then
+// handed to fp32 sine and cosine, so that positions far out lose nothing.
+//
+// The step is bound by its bytes (the queries of all heads make nearly all of
+// them) at prompt lengths and by one launch's latency for single tokens.
+// Two kinds of CTAs share one launch:
+//   rows:  a few rows each, one 16-byte chunk (or the two halves of a pair of
+//          chunks) per thread and turn; cosines and sines once a row in shared
+//          memory, used by all of its heads.  With a 16-bit cache the key is one
+//          more head of the row, value and index key are copied beside it.
+//   pages: (8-bit caches) the new tokens of one 64-token page, so that every
+//          scale block has one owner whatever its length: a warp holds a
+//          token's key and value in registers (d / 32 values a lane, pair
+//          partners exchanged by shuffles), block maxima meet in shared memory,
+//          and codes are made from the registers once the scales are known.
+#include <algorithm>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace sa {
+
+namespace {
+
+constexpr int kAThreads = 256;
+constexpr int kARowsMax = 8;        // rows of one row CTA
+constexpr int kAPage = 64;
+
+struct AppendParams {
+    AppendArgs a;
+    int n_page_ctas;     // CTAs of the page kind, first in the grid (8-bit caches)
+    int jobs;            // page CTAs a sequence
+    int rows;            // rows per row CTA
+    int heads;           // heads a row CTA rotates: Hq, and the key with a 16-bit cache
+    int u_rot, u_head;   // rotating chunks (or chunk pairs) and all units of a head
+    int u_row;           // units of a row
+    uint32_t m_head, m_row;   // ceil(2^16 / u_head), ceil(2^24 / u_row)
+};
+
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+// cos and sin of p * f (see the head of the file)
+__device__ __forceinline__ float2 turn(int p, float f) {
+    const double t = (double)p * (double)f * 0.15915494309189535;
+    const float x = (float)(2.0 * (t - rint(t)));   // the angle in half turns, -1 .. 1
+    float2 cs;
+    sincospif(x, &cs.y, &cs.x);
+    return cs;
+}
+
+// Cache row of position p (within the cache) of sequence b; -1 for a bad page id.
+__device__ __forceinline__ int64_t cache_slot(const AppendArgs &a, int b, int p) {
+    if (!a.page_table) return (int64_t)b * a.S_max + p;
+    const int page = a.page_table[(int64_t)b * a.max_pages + p / kAPage];
+    if (page < 0 || page >= a.pool_pages) return -1;
+    return (int64_t)page * kAPage + p % kAPage;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    unsigned short r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)c));
+    float2 f;
+    asm("{ .reg .b16 l, u; mov.b32 {l, u}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, u; }" : "=f"(f.x), "=f"(f.y) : "r"(h));
+    return f;
+}
+__device__ __forceinline__ uint2 e4m3_of8(const uint4 &u) {
+    uint2 o;
+    o.x = e4m3x2(bf_lo(u.x), bf_hi(u.x)) | e4m3x2(bf_lo(u.y), bf_hi(u.y)) << 16;
+    o.y = e4m3x2(bf_lo(u.z), bf_hi(u.z)) | e4m3x2(bf_lo(u.w), bf_hi(u.w)) << 16;
+    return o;
+}
+
+// The smallest 2^e, -64 <= e <= 64, with amax <= 448 * 2^e (448 = 0.875 * 2^9).
+__device__ __forceinline__ float scale_for(float amax) {
+    if (!(amax > 0.f)) return 5.421010862427522e-20f;   // 2^-64
+    int x;
+    const float m = frexpf(amax, &x);
+    const int e = min(64, max(-64, m <= 0.875f ? x - 9 : x - 8));
+    return __int_as_float((e + 127) << 23);
+}
+__device__ __forceinline__ float clamp_scale(float s) {   // NaN -> 2^-64
+    return fminf(fmaxf(s, 5.421010862427522e-20f), 1.8446744073709552e19f);
+}
+
+// ------------------------------------------------------------------ rows
+// One chunk pair (halves) or chunk (interleaved) of 8 values, rotated.
+template <bool INTER>
+__device__ __forceinline__ void rotate8(uint4 &a, uint4 &b, const float2 *cs) {
+    uint32_t *x = reinterpret_cast<uint32_t *>(&a), *y = reinterpret_cast<uint32_t *>(&b);
+    if (INTER) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float u = bf_lo(x[i]), v = bf_hi(x[i]);
+            x[i] = pack_bf16(u * cs[i].x - v * cs[i].y, v * cs[i].x + u * cs[i].y);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float u0 = bf_lo(x[i]), u1 = bf_hi(x[i]), v0 = bf_lo(y[i]), v1 = bf_hi(y[i]);
+            const float2 c0 = cs[2 * i], c1 = cs[2 * i + 1];
+            x[i] = pack_bf16(u0 * c0.x - v0 * c0.y, u1 * c1.x - v1 * c1.y);
+            y[i] = pack_bf16(v0 * c0.x + u0 * c0.y, v1 * c1.x + u1 * c1.y);
+        }
+    }
+}
+
+template <bool INTER>
+__device__ void append_rows(const AppendParams &P, int cta, float2 (*cs)[64], int64_t *slot, int *pos) {
+    const AppendArgs &a = P.a;
+    const int R = a.B * a.T, r0 = cta * P.rows, nr = min(P.rows, R - r0), half = a.rot_dim / 2;
+    if (threadIdx.x < nr) {
+        const int r = r0 + threadIdx.x, n = a.n_valid[r];
+        int p = n - 1;
+        int64_t s = -1;
+        if (n < 0 || n > a.S_max) {
+            report(a.dev_status, SA_DEV_INDEX);
+            p = -1;
+        } else if (p >= 0 && !a.q8) {
+            s = cache_slot(a, r / a.T, p);
+            if (s < 0) report(a.dev_status, SA_DEV_INDEX);
+        }
+        pos[threadIdx.x] = p;
+        slot[threadIdx.x] = s;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < nr * half; i += kAThreads) {
+        const int rl = i / half, f = i - rl * half;
+        if (pos[rl] >= 0) cs[rl][f] = turn(pos[rl], __ldg(a.inv_freq + f));
+    }
+    __syncthreads();
+    const int u_heads = P.heads * P.u_head;
+    for (int i = threadIdx.x; i < nr * P.u_row; i += kAThreads) {
+        const int rl = (int)(((uint64_t)i * P.m_row) >> 24), u = i - rl * P.u_row;
+        if (pos[rl] < 0) continue;
+        const int64_t r = r0 + rl;
+        if (u < u_heads) {
+            const int h = (int)((u * P.m_head) >> 16), c = u - h * P.u_head;
+            const bool is_k = h == a.Hq;   // the row's key (16-bit cache)
+            if (is_k && slot[rl] < 0) continue;
+            const uint16_t *src = is_k ? a.k + r * a.ld_k : a.q + r * a.ld_q + h * a.d;
+            uint16_t *dst = is_k ? static_cast<uint16_t *>(a.k_cache) + slot[rl] * a.d : a.q_out + (r * a.Hq + h) * a.d;
+            if (c < P.u_rot) {
+                uint4 x = *reinterpret_cast<const uint4 *>(src + c * 8), y = make_uint4(0, 0, 0, 0);
+                if (!INTER) y = *reinterpret_cast<const uint4 *>(src + half + c * 8);
+                rotate8<INTER>(x, y, &cs[rl][INTER ? 4 * c : 8 * c]);
+                *reinterpret_cast<uint4 *>(dst + c * 8) = x;
+                if (!INTER) *reinterpret_cast<uint4 *>(dst + half + c * 8) = y;
+            } else {
+                const int o = a.rot_dim + (c - P.u_rot) * 8;
+                *reinterpret_cast<uint4 *>(dst + o) = *reinterpret_cast<const uint4 *>(src + o);
+            }
+        } else if (slot[rl] >= 0) {
+            const int c = (u - u_heads) * 8;
+            if (c < a.d) {
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.v_cache) + slot[rl] * a.d + c) =
+                    *reinterpret_cast<const uint4 *>(a.v + r * a.ld_v + c);
+            } else {
+                const uint4 x = *reinterpret_cast<const uint4 *>(a.kI + r * a.ld_kI + (c - a.d));
+                const int64_t o = slot[rl] * a.D_I + (c - a.d);
+                if (a.kI_e4m3)
+                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.kI_cache) + o) = e4m3_of8(x);
+                else
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.kI_cache) + o) = x;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ pages
+// The scale and codes of one side (keys or values) of the page's new tokens.
+template <int NV>
+__device__ __forceinline__ void store_codes(uint8_t *dst, int lane, const float (&x)[NV], float s) {
+    if (NV == 4)
+        *reinterpret_cast<uint32_t *>(dst + lane * 4) =
+            e4m3x2(__fdiv_rn(x[0], s), __fdiv_rn(x[1], s)) | e4m3x2(__fdiv_rn(x[NV - 2], s), __fdiv_rn(x[NV - 1], s)) << 16;
+    else
+        *reinterpret_cast<uint16_t *>(dst + lane * 2) = (uint16_t)e4m3x2(__fdiv_rn(x[0], s), __fdiv_rn(x[1], s));
+}
+
+__device__ __forceinline__ uint32_t finite_abs(float x) {   // bits of |x|, 0 for infinities and NaN
+    const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
+    return b < 0x7F800000u ? b : 0u;
+}
+
+template <int D, bool INTER>
+__device__ void append_page(const AppendParams &P, int job, uint32_t (*amax)[kAPage], float (*scale)[kAPage], int *red,
+                            float *ratio) {
+    constexpr int NV = D / 32, NW = kAThreads / 32, NT = kAPage / NW;   // values a lane, warps, tokens a warp
+    const AppendArgs &a = P.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int b = job / P.jobs, j = job - b * P.jobs;
+    const int32_t *nv = a.n_valid + (int64_t)b * a.T;
+
+    // the sequence's run of valid rows, checked: red = first, last, count, errors
+    if (tid < 4) red[tid] = tid == 0 ? a.T : (tid == 1 ? -1 : 0);
+    for (int i = tid; i < 2 * kAPage; i += kAThreads) amax[i / kAPage][i % kAPage] = 0;
+    __syncthreads();
+    int first = a.T, last = -1, count = 0, err = 0;
+    for (int t = tid; t < a.T; t += kAThreads) {
+        const int n = __ldg(nv + t);
+        if (n < 0 || n > a.S_max) err |= SA_DEV_INDEX;
+        if (n > 0) {
+            const int before = t > 0 ? __ldg(nv + t - 1) : 0;
+            if (before > 0 && n != before + 1) err |= SA_DEV_ORDER;
+            first = min(first, t);
+            last = max(last, t);
+            ++count;
+        }
+    }
+    if (last >= 0) {
+        atomicMin(&red[0], first);
+        atomicMax(&red[1], last);
+        atomicAdd(&red[2], count);
+    }
+    if (err) atomicOr(&red[3], err);
+    __syncthreads();
+    first = red[0];
+    count = red[2];
+    err = red[3];
+    if (count > 0 && red[1] - first + 1 != count) err |= SA_DEV_ORDER;   // a gap
+    if (err & SA_DEV_INDEX) err = SA_DEV_INDEX;   // a number out of range is no successor either: one error
+    if (err || count == 0) {
+        if (err && j == 0 && tid == 0) report(a.dev_status, err);
+        return;
+    }
+    const int p0 = __ldg(nv + first) - 1, page = p0 / kAPage + j;
+    const int begin = max(p0, page * kAPage), m = min(p0 + count, (page + 1) * kAPage) - begin;
+    if (m <= 0) return;
+    const int64_t base = cache_slot(a, b, page * kAPage);   // the page's first slot
+    if (base < 0) {
+        if (tid == 0) report(a.dev_status, SA_DEV_INDEX);
+        return;
+    }
+    const int o0 = begin % kAPage, sb = a.scale_block;
+    const int64_t row0 = (int64_t)b * a.T + first + (begin - p0);
+
+    // keys (rotated) and values of this warp's tokens warp, warp + NW, ...
+    const int half = a.rot_dim / 2, hl = half / NV;      // lanes of one half of the rotated dims
+    const int d0 = lane * NV;                            // this lane's first dim
+    const bool rot = d0 < a.rot_dim;
+    const int partner = INTER ? lane : (lane < hl ? lane + hl : (lane < 2 * hl ? lane - hl : lane));
+    const bool upper = !INTER && lane >= hl;
+    float kx[NT][NV], vx[NT][NV];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int tok = i * NW + warp;
+        if (tok >= m) break;   // the same for the whole warp
+        const uint16_t *kr = a.k + (row0 + tok) * a.ld_k + d0, *vr = a.v + (row0 + tok) * a.ld_v + d0;
+        uint32_t kw[NV / 2], vw[NV / 2];
+#pragma unroll
+        for (int e = 0; e < NV / 2; ++e) {
+            kw[e] = __ldg(reinterpret_cast<const uint32_t *>(kr) + e);
+            vw[e] = __ldg(reinterpret_cast<const uint32_t *>(vr) + e);
+        }
+        float x[NV];
+#pragma unroll
+        for (int e = 0; e < NV / 2; ++e) {
+            x[2 * e] = bf_lo(kw[e]);
+            x[2 * e + 1] = bf_hi(kw[e]);
+            vx[i][2 * e] = bf_lo(vw[e]);
+            vx[i][2 * e + 1] = bf_hi(vw[e]);
+        }
+        if (INTER) {
+#pragma unroll
+            for (int e = 0; e < NV / 2; ++e) {
+                const float2 c = rot ? turn(begin + tok, __ldg(a.inv_freq + d0 / 2 + e)) : make_float2(1.f, 0.f);
+                kx[i][2 * e] = rot ? x[2 * e] * c.x - x[2 * e + 1] * c.y : x[2 * e];
+                kx[i][2 * e + 1] = rot ? x[2 * e + 1] * c.x + x[2 * e] * c.y : x[2 * e + 1];
+            }
+        } else {
+            // the pair's two lanes need the same NV angles: each takes half of them
+            const int f0 = (upper ? d0 - half : d0);
+            float2 mine[NV / 2];
+#pragma unroll
+            for (int e = 0; e < NV / 2; ++e)
+                mine[e] = rot ? turn(begin + tok, __ldg(a.inv_freq + f0 + (upper ? NV / 2 : 0) + e)) : make_float2(1.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < NV / 2; ++e) {
+                const float2 other = make_float2(__shfl_sync(0xffffffffu, mine[e].x, partner),
+                                                 __shfl_sync(0xffffffffu, mine[e].y, partner));
+                const float2 c0 = upper ? other : mine[e], c1 = upper ? mine[e] : other;   // angles e and NV / 2 + e
+                const float y0 = __shfl_sync(0xffffffffu, x[e], partner);
+                const float y1 = __shfl_sync(0xffffffffu, x[NV / 2 + e], partner);
+                const float s0 = upper ? c0.y : -c0.y, s1 = upper ? c1.y : -c1.y;
+                kx[i][e] = rot ? x[e] * c0.x + y0 * s0 : x[e];
+                kx[i][NV / 2 + e] = rot ? x[NV / 2 + e] * c1.x + y1 * s1 : x[NV / 2 + e];
+            }
+        }
+        uint32_t mk = 0, mv = 0;
+#pragma unroll
+        for (int e = 0; e < NV; ++e) {
+            mk = max(mk, finite_abs(kx[i][e]));
+            mv = max(mv, finite_abs(vx[i][e]));
+        }
+        mk = __reduce_max_sync(0xffffffffu, mk);
+        mv = __reduce_max_sync(0xffffffffu, mv);
+        if (lane == 0) {   // non-negative floats order as their bits
+            atomicMax(&amax[0][(o0 + tok) / sb], mk);
+            atomicMax(&amax[1][(o0 + tok) / sb], mv);
+        }
+    }
+    if (a.kI) {   // index keys beside them
+        const int nc = a.D_I / 8;
+        for (int i = tid; i < m * nc; i += kAThreads) {
+            const int tok = i / nc, c = (i - tok * nc) * 8;
+            const uint4 x = *reinterpret_cast<const uint4 *>(a.kI + (row0 + tok) * a.ld_kI + c);
+            const int64_t o = (base + o0 + tok) * a.D_I + c;
+            if (a.kI_e4m3)
+                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.kI_cache) + o) = e4m3_of8(x);
+            else
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.kI_cache) + o) = x;
+        }
+    }
+    __syncthreads();
+    // scales of the touched blocks; ratio: what the first block's earlier tokens shrink by
+    if (tid < 2) ratio[tid] = 1.f;
+    __syncthreads();
+    const int blk0 = o0 / sb, blk1 = (o0 + m - 1) / sb;
+    const int64_t sbase = base / sb;
+    for (int i = tid; i < 2 * kAPage; i += kAThreads) {
+        const int side = i / kAPage, blk = i % kAPage;
+        if (blk >= blk0 && blk <= blk1) {
+            float *ps = (side ? a.v_scale : a.k_scale) + sbase + blk;
+            float s = scale_for(__uint_as_float(amax[side][blk]));
+            if (blk * sb < o0) {   // the block holds earlier tokens
+                const float was = *ps, old = clamp_scale(was);
+                s = fmaxf(s, old);
+                ratio[side] = s == old ? 1.f : __fdiv_rn(old, s);
+            }
+            scale[side][blk] = s;
+            *ps = s;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int tok = i * NW + warp;
+        if (tok >= m) break;
+        const int blk = (o0 + tok) / sb;
+        const int64_t o = (base + o0 + tok) * D;
+        store_codes<NV>(static_cast<uint8_t *>(a.k_cache) + o, lane, kx[i], scale[0][blk]);
+        store_codes<NV>(static_cast<uint8_t *>(a.v_cache) + o, lane, vx[i], scale[1][blk]);
+    }
+    // earlier tokens of a block whose scale grew
+    const int words = (o0 - blk0 * sb) * (D / 4);
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        const float f = ratio[side];
+        if (f == 1.f) continue;
+        uint32_t *w = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(side ? a.v_cache : a.k_cache) +
+                                                   (base + blk0 * sb) * D);
+        for (int i = tid; i < words; i += kAThreads) {
+            const uint32_t c = w[i];
+            const float2 lo = from_e4m3x2(c & 0xFFFFu), hi = from_e4m3x2(c >> 16);
+            w[i] = e4m3x2(lo.x * f, lo.y * f) | e4m3x2(hi.x * f, hi.y * f) << 16;
+        }
+    }
+}
+
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kAThreads) append_kernel(AppendParams P) {
+    __shared__ float2 cs[kARowsMax][64];
+    __shared__ int64_t slot[kARowsMax];
+    __shared__ int pos[kARowsMax];
+    __shared__ uint32_t amax[2][kAPage];
+    __shared__ float scale[2][kAPage], ratio[2];
+    __shared__ int red[4];
+    if ((int)blockIdx.x < P.n_page_ctas)
+        append_page<D, INTER>(P, (int)blockIdx.x, amax, scale, red, ratio);
+    else
+        append_rows<INTER>(P, (int)blockIdx.x - P.n_page_ctas, cs, slot, pos);
+}
+
+}  // namespace
+
+sa_status launch_append(const AppendArgs &a, cudaStream_t st) {
+    AppendParams P;
+    P.a = a;
+    const int64_t R = (int64_t)a.B * a.T;
+    P.jobs = (a.T + 62) / kAPage + 1;   // pages that T consecutive tokens can touch
+    const int64_t n_page = a.q8 ? (int64_t)a.B * P.jobs : 0;
+    P.heads = a.q8 ? a.Hq : a.Hq + 1;
+    P.u_rot = a.interleaved ? a.rot_dim / 8 : a.rot_dim / 16;
+    P.u_head = P.u_rot + (a.d - a.rot_dim) / 8;
+    P.u_row = P.heads * P.u_head + (a.q8 ? 0 : (a.d + a.D_I) / 8);
+    P.rows = P.u_row > 0 ? std::min(kARowsMax, std::max(1, kAThreads / P.u_row)) : 1;
+    P.m_head = (65536u + P.u_head - 1) / P.u_head;
+    P.m_row = P.u_row > 0 ? ((1u << 24) + P.u_row - 1) / P.u_row : 0;
+    const int64_t n_rows = P.u_row > 0 ? (R + P.rows - 1) / P.rows : 0;
+    if (n_page + n_rows > INT32_MAX) return SA_ERR_UNSUPPORTED;
+    P.n_page_ctas = (int)n_page;
+    const unsigned grid = (unsigned)(n_page + n_rows);
+    if (grid == 0) return SA_OK;
+    if (a.d == 128) {
+        if (a.interleaved) append_kernel<128, true><<<grid, kAThreads, 0, st>>>(P);
+        else append_kernel<128, false><<<grid, kAThreads, 0, st>>>(P);
+    } else {
+        if (a.interleaved) append_kernel<64, true><<<grid, kAThreads, 0, st>>>(P);
+        else append_kernel<64, false><<<grid, kAThreads, 0, st>>>(P);
+    }
+    return cuda_ok(cudaGetLastError());
+}
+
+}  // namespace sa

@@ -250,6 +250,88 @@ sa_status sa_sparse_attn_decode(const sa_bf16 *q, const sa_bf16 *k_cache, const 
     });
 }
 
+// Shared by the 16- and 8-bit appends (scales NULL and scale_block 1 for 16 bits).
+static sa_status cache_append(const sa_bf16 *q, int64_t ld_q, sa_bf16 *q_out, const sa_bf16 *k, int64_t ld_k,
+                              const sa_bf16 *v, int64_t ld_v, const sa_bf16 *kI, int64_t ld_kI, const int32_t *n_valid,
+                              const int32_t *page_table, int max_pages, int pool_pages, int page_size, int S_max, int B,
+                              int T, int Hq, int d, int D_I, const float *inv_freq, int rot_dim, int interleaved,
+                              void *k_cache, void *v_cache, float *k_scale, float *v_scale, int scale_block, bool q8,
+                              void *kI_cache, int kI_e4m3, int *dev_status, sa_stream stream) {
+    if (B < 0 || T < 0 || ld_q < 0 || ld_k < 0 || ld_v < 0 || ld_kI < 0) return SA_ERR_INVALID_ARG;
+    if (!head_dim_ok(d) || rot_dim < 0 || rot_dim > d || rot_dim % 16) return SA_ERR_UNSUPPORTED;
+    if ((q == nullptr) != (q_out == nullptr) || (kI == nullptr) != (kI_cache == nullptr)) return SA_ERR_INVALID_ARG;
+    if (q && (Hq < 1 || Hq > 64)) return SA_ERR_UNSUPPORTED;
+    if (kI && !(D_I == 32 || D_I == 64 || D_I == 128)) return SA_ERR_UNSUPPORTED;
+    const sa_status chk = check_cache_shape(page_table, max_pages, pool_pages, page_size, S_max, B, scale_block);
+    if (chk != SA_OK) return chk;
+    if ((int64_t)B * T > (1 << 30)) return SA_ERR_UNSUPPORTED;
+    if (B == 0 || T == 0) return SA_OK;
+    if (!k || !v || !k_cache || !v_cache || !n_valid || (q8 && (!k_scale || !v_scale)) || (rot_dim > 0 && !inv_freq))
+        return SA_ERR_INVALID_ARG;
+    if ((q && (ld_q < (int64_t)Hq * d || (ld_q & 7))) || ld_k < d || (ld_k & 7) || ld_v < d || (ld_v & 7) ||
+        (kI && (ld_kI < D_I || (ld_kI & 7))) || (q && q == q_out && ld_q != (int64_t)Hq * d))
+        return SA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v) || !aligned16(kI) || !aligned16(k_cache) ||
+        !aligned16(v_cache) || !aligned16(kI_cache))
+        return SA_ERR_INVALID_ARG;
+    return guarded([&] {
+        AppendArgs a;
+        a.q = q; a.k = k; a.v = v; a.kI = kI; a.ld_q = ld_q; a.ld_k = ld_k; a.ld_v = ld_v; a.ld_kI = ld_kI;
+        a.q_out = q_out; a.n_valid = n_valid; a.page_table = page_table; a.max_pages = max_pages;
+        a.pool_pages = pool_pages; a.S_max = page_table ? max_pages * 64 : S_max;
+        a.B = B; a.T = T; a.Hq = q ? Hq : 0; a.d = d; a.D_I = kI ? D_I : 0; a.inv_freq = inv_freq; a.rot_dim = rot_dim;
+        a.interleaved = interleaved != 0; a.q8 = q8; a.kI_e4m3 = kI_e4m3 != 0;
+        a.k_cache = k_cache; a.v_cache = v_cache; a.kI_cache = kI_cache; a.k_scale = k_scale; a.v_scale = v_scale;
+        a.scale_block = scale_block; a.dev_status = dev_status;
+        return launch_append(a, cs(stream));
+    });
+}
+
+sa_status sa_cache_append(const sa_bf16 *q, int64_t ld_q, sa_bf16 *q_out, const sa_bf16 *k, int64_t ld_k,
+                          const sa_bf16 *v, int64_t ld_v, const sa_bf16 *kI, int64_t ld_kI, const int32_t *n_valid,
+                          const int32_t *page_table, int max_pages, int pool_pages, int page_size, int S_max, int B,
+                          int T, int Hq, int d, int D_I, const float *inv_freq, int rot_dim, int interleaved,
+                          sa_bf16 *k_cache, sa_bf16 *v_cache, void *kI_cache, int kI_e4m3, int *dev_status,
+                          sa_stream stream) {
+    return cache_append(q, ld_q, q_out, k, ld_k, v, ld_v, kI, ld_kI, n_valid, page_table, max_pages, pool_pages,
+                        page_size, S_max, B, T, Hq, d, D_I, inv_freq, rot_dim, interleaved, k_cache, v_cache, nullptr,
+                        nullptr, 1, false, kI_cache, kI_e4m3, dev_status, stream);
+}
+
+sa_status sa_cache_append_q8(const sa_bf16 *q, int64_t ld_q, sa_bf16 *q_out, const sa_bf16 *k, int64_t ld_k,
+                             const sa_bf16 *v, int64_t ld_v, const sa_bf16 *kI, int64_t ld_kI, const int32_t *n_valid,
+                             const int32_t *page_table, int max_pages, int pool_pages, int page_size, int S_max, int B,
+                             int T, int Hq, int d, int D_I, const float *inv_freq, int rot_dim, int interleaved,
+                             sa_e4m3 *k_cache, sa_e4m3 *v_cache, float *k_scale, float *v_scale, int scale_block,
+                             void *kI_cache, int kI_e4m3, int *dev_status, sa_stream stream) {
+    return cache_append(q, ld_q, q_out, k, ld_k, v, ld_v, kI, ld_kI, n_valid, page_table, max_pages, pool_pages,
+                        page_size, S_max, B, T, Hq, d, D_I, inv_freq, rot_dim, interleaved, k_cache, v_cache, k_scale,
+                        v_scale, scale_block, true, kI_cache, kI_e4m3, dev_status, stream);
+}
+
+sa_status sa_sparse_attn_q8(const sa_bf16 *q, const sa_e4m3 *k_cache, const sa_e4m3 *v_cache, const float *k_scale,
+                            const float *v_scale, int scale_block, const int32_t *page_table, int max_pages,
+                            int pool_pages, int page_size, int S_max, const int32_t *n_valid, const int32_t *topk, int K,
+                            int W, int B, int T, int Hq, int d, float scale, sa_bf16 *out, float *lse, int *dev_status,
+                            sa_stream stream) {
+    if (K < 0 || W < 0 || B < 0 || T < 0 || K + (int64_t)W == 0) return SA_ERR_INVALID_ARG;
+    if (!head_dim_ok(d) || Hq < 1 || Hq > 64 || K + (int64_t)W > 524288) return SA_ERR_UNSUPPORTED;
+    const sa_status chk = check_cache_shape(page_table, max_pages, pool_pages, page_size, S_max, B, scale_block);
+    if (chk != SA_OK) return chk;
+    if ((int64_t)B * T > (1 << 26)) return SA_ERR_UNSUPPORTED;
+    if (B == 0 || T == 0) return SA_OK;
+    if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !n_valid || !out || (K > 0 && !topk)) return SA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return SA_ERR_INVALID_ARG;
+    return guarded([&] {
+        AttnQ8Args a;
+        a.q = q; a.k = k_cache; a.v = v_cache; a.k_scale = k_scale; a.v_scale = v_scale; a.scale_block = scale_block;
+        a.page_table = page_table; a.max_pages = max_pages; a.pool_pages = pool_pages;
+        a.S_max = page_table ? max_pages * 64 : S_max; a.n_valid = n_valid; a.topk = topk; a.K = K; a.W = W; a.B = B;
+        a.T = T; a.Hq = Hq; a.d = d; a.scale = scale; a.out = out; a.lse = lse; a.dev_status = dev_status;
+        return launch_attn_q8(a, cs(stream));
+    });
+}
+
 sa_status sa_pool_index_keys(const sa_bf16 *kI, int S, int D_I, int block, sa_bf16 *kB, sa_stream stream) {
     if (S < 0 || block <= 0) return SA_ERR_INVALID_ARG;
     if (!index_dim_ok(D_I)) return SA_ERR_UNSUPPORTED;

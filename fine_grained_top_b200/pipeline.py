@@ -6,7 +6,11 @@ library's kernels on one stream; the host does no arithmetic of the method.
     PrefillPlan    indexer -> top-K -> sparse attention for one causal
                    sequence (optionally the two-stage coarse/fine selection)
     DecodePlan     one new query per sequence over a contiguous or paged
-                   KV cache: indexer -> top-K -> split-K attention + merge
+                   KV cache: indexer -> top-K -> split-K attention + merge;
+                   over an 8-bit cache also a chunk of T queries per sequence
+    KVCache        the caches of B sequences (16 or 8 bits) and the append
+                   that fills them with rotated keys, a first stage of a
+                   DecodePlan that is given one
     HostPipeline   steps fed from and read back to pinned host memory, the
                    copies of neighbouring steps overlapped with the kernels
 
@@ -20,10 +24,12 @@ import math
 
 import torch
 
-from . import (sa_block_scores_workspace_bytes, sa_coarse_block_counts, sa_decode_workspace_bytes,
+from . import (sa_block_scores_workspace_bytes, sa_cache_append, sa_cache_append_q8, sa_coarse_block_counts,
+               sa_decode_workspace_bytes,
                sa_indexer_scores, sa_indexer_scores_blocks, sa_indexer_scores_fp8, sa_indexer_topk_decode,
                sa_pool_index_keys,
-               sa_prefill_workspace_bytes, sa_sparse_attn_decode, sa_sparse_attn_prefill, sa_topk_select,
+               sa_prefill_workspace_bytes, sa_sparse_attn_decode, sa_sparse_attn_prefill,
+               sa_sparse_attn_q8, sa_topk_select,
                sa_topk_select_blocks)
 
 
@@ -140,15 +146,106 @@ class PrefillPlan:
         return (2 * self.row_blocks if self.block is None else 9) + attn
 
 
+class KVCache:
+    """The caches of B sequences: keys and values of the one KV head and index
+    keys, contiguous ([B, S_max, *]) or pools of 64-token pages ([pool_pages,
+    64, *], addressed by the page table that append() and the plans are given).
+
+    q8: keys and values in e4m3 with one power-of-two scale for each
+    scale_block tokens (else bf16); index_fp8: e4m3 index keys.
+    Positions: pairs of the first rot_dim dims (default all) turn by
+    p * inv_freq[i]; inv_freq defaults to theta^(-2i / rot_dim).
+    interleaved: pairs (2i, 2i + 1) instead of (i, i + rot_dim / 2)."""
+
+    def __init__(self, B, d, D_I, S_max=0, paged=False, max_pages=0, pool_pages=0, q8=False, scale_block=64,
+                 index_fp8=False, rot_dim=None, theta=10000.0, inv_freq=None, interleaved=False, device="cuda"):
+        self.B, self.d, self.D_I, self.paged, self.q8, self.scale_block = B, d, D_I, paged, q8, scale_block
+        self.max_pages, self.pool_pages = (max_pages, pool_pages) if paged else (0, 0)
+        self.S_max = max_pages * 64 if paged else S_max
+        self.index_fp8, self.interleaved = index_fp8, interleaved
+        self.rot_dim = d if rot_dim is None else rot_dim
+        if q8 and not (1 <= scale_block <= 64 and scale_block & (scale_block - 1) == 0 and self.S_max % scale_block == 0):
+            raise ValueError("scale_block is a power of two up to 64 that divides the cache's length")
+        dev = torch.device(device)
+        if inv_freq is None:
+            i = torch.arange(self.rot_dim // 2, dtype=torch.float64)
+            inv_freq = (theta ** (-2 * i / max(self.rot_dim, 1))).float()
+        self.inv_freq = inv_freq.to(device=dev, dtype=torch.float32).contiguous()
+        if self.inv_freq.numel() < self.rot_dim // 2:
+            raise ValueError("inv_freq needs rot_dim / 2 entries")
+        lead = (pool_pages, 64) if paged else (B, S_max)
+        kv, index = torch.uint8 if q8 else torch.bfloat16, torch.uint8 if index_fp8 else torch.bfloat16
+        self.k = torch.zeros(lead + (d,), dtype=kv, device=dev)
+        self.v = torch.zeros(lead + (d,), dtype=kv, device=dev)
+        self.kI = torch.zeros(lead + (D_I,), dtype=index, device=dev)
+        self.k_scale = self.v_scale = None
+        if q8:
+            blocks = (lead[0], lead[1] // scale_block)
+            self.k_scale = torch.ones(blocks, dtype=torch.float32, device=dev)
+            self.v_scale = torch.ones(blocks, dtype=torch.float32, device=dev)
+        self.dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    @staticmethod
+    def _rows(t, R, width):
+        """(tensor, row stride) of R rows of `width` values: contiguous, or slices of wider rows."""
+        if t is None:
+            return None, 0
+        if t.is_contiguous():
+            return t, width
+        if t.dim() != 2 or tuple(t.shape) != (R, width) or t.stride(1) != 1:
+            raise ValueError("new rows are contiguous, or [rows, %d] slices of wider rows" % width)
+        return t, t.stride(0)
+
+    def append(self, q, k, v, kI, n_valid, T=1, page_table=None, q_out=None, stream=None, dev_status=None):
+        """Write the new tokens' rotated keys, values and index keys ([B*T, *])
+        to their slots (row b*T + t at position n_valid[b*T + t] - 1, 0:
+        padding) and return the rotated queries (q [B*T, Hq, d], q_out or a new
+        tensor; None when q is None)."""
+        R, d = self.B * T, self.d
+        Hq = q.numel() // (R * d) if q is not None and R > 0 else 1
+        if q is not None and q_out is None:
+            q_out = torch.zeros((R, Hq, d), dtype=torch.bfloat16, device=q.device)
+        (q, ld_q), (k, ld_k) = self._rows(q, R, Hq * d), self._rows(k, R, d)
+        (v, ld_v), (kI, ld_kI) = self._rows(v, R, d), self._rows(kI, R, self.D_I)
+        status = self.dev_status if dev_status is None else dev_status
+        rows = (q, ld_q, q_out, k, ld_k, v, ld_v, kI, ld_kI, n_valid, page_table if self.paged else None, self.max_pages,
+                self.pool_pages, 64, self.S_max, self.B, T, Hq, d, self.D_I, self.inv_freq, self.rot_dim,
+                int(self.interleaved), self.k, self.v)
+        index = (self.kI if kI is not None else None, int(self.index_fp8), status, stream)
+        if self.q8:
+            sa_cache_append_q8(*rows, self.k_scale, self.v_scale, self.scale_block, *index)
+        else:
+            sa_cache_append(*rows, *index)
+        return q_out
+
+
 class DecodePlan:
     """Buffers for B sequences, one query each, over a contiguous ([B, S_max, *])
     or paged (pools [P, 64, *] + page_table [B, max_pages]) cache.
     Inputs: dict with q [B,Hq,d], k/v/kI caches, qI [B,H_I,D_I], w [B,H_I],
     lengths [B] int32 and, when paged, page_table.
-    index_fp8: the qI and kI cache hold e4m3 bytes (uint8); FP8 indexer."""
+    index_fp8: the qI and kI cache hold e4m3 bytes (uint8); FP8 indexer.
+    kv_q8: k and v are 8-bit caches (uint8) and the inputs hold k_scale and
+    v_scale too, one for each scale_block tokens; T queries per sequence (rows
+    b*T + t of q, qI and w), and lengths [B*T] gives the cached tokens that each
+    of them sees (0: padding).
+    cache: a KVCache.  Each step then begins by appending its tokens: the inputs
+    k, v and kI are the new tokens' rows [B*T, *] and q is not yet rotated; kv_q8,
+    scale_block, index_fp8 (for kI; qI is e4m3 too then) and the cache's sizes
+    are taken from it."""
 
-    def __init__(self, B, Hq, d, H_I, D_I, K, W, S_max, paged=False, max_pages=0, pool_pages=0,
-                 index_fp8=False, fused=None, device="cuda"):
+    def __init__(self, B, Hq, d, H_I, D_I, K, W, S_max=0, paged=False, max_pages=0, pool_pages=0,
+                 index_fp8=False, fused=None, device="cuda", kv_q8=False, scale_block=64, T=1, cache=None):
+        if cache is not None:
+            if (cache.B, cache.d, cache.D_I) != (B, d, D_I):
+                raise ValueError("the cache holds other sequences or dims than the plan")
+            paged, max_pages, pool_pages, S_max = cache.paged, cache.max_pages, cache.pool_pages, cache.S_max
+            kv_q8, scale_block, index_fp8 = cache.q8, cache.scale_block, cache.index_fp8
+        if T != 1 and not kv_q8:
+            raise ValueError("several queries per sequence need the 8-bit cache's attention (kv_q8)")
+        if T < 1:
+            raise ValueError("a step has at least one query per sequence")
+        self.kv_q8, self.scale_block, self.T, self.cache = kv_q8, scale_block, T, cache
         self.B, self.Hq, self.d, self.H_I, self.D_I, self.K, self.W = B, Hq, d, H_I, D_I, K, W
         self.index = sa_indexer_scores_fp8 if index_fp8 else sa_indexer_scores
         self.paged, self.max_pages, self.pool_pages = paged, max_pages, pool_pages
@@ -162,22 +259,32 @@ class DecodePlan:
         # about half the separate indexer's rate).
         fusable = not index_fp8 and H_I <= 8 and D_I in (64, 128) and self.S <= 262144
         self.fused = False if fused is None else bool(fused)
+        if self.fused and T != 1:
+            raise ValueError("the fused indexer + top-K takes one query per sequence")
         if self.fused and not fusable:
             raise ValueError("the fused indexer + top-K takes bf16 operands, H_I <= 8, D_I in (64, 128) and "
                              "rows of at most 262144 keys")
         self.scale = 1.0 / math.sqrt(d)
         dev = torch.device(device)
+        R = B * T
         self.ld = _ld(self.S)
-        self.scores = None if self.fused else torch.empty((B, self.ld), dtype=torch.float32, device=dev)
-        self.topk = torch.empty((B, K), dtype=torch.int32, device=dev)
-        self.out = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=dev)
-        self.lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-        self.ws_bytes = sa_decode_workspace_bytes(B, Hq, d, K, W)
+        self.scores = None if self.fused else torch.empty((R, self.ld), dtype=torch.float32, device=dev)
+        self.topk = torch.empty((R, K), dtype=torch.int32, device=dev)
+        self.out = torch.empty((R, Hq, d), dtype=torch.bfloat16, device=dev)
+        self.lse = torch.empty((R, Hq), dtype=torch.float32, device=dev)
+        self.q_rot = torch.zeros((R, Hq, d), dtype=torch.bfloat16, device=dev) if cache is not None else None
+        self.ws_bytes = 0 if kv_q8 else sa_decode_workspace_bytes(B, Hq, d, K, W)   # the 8-bit attention has none
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
 
     def stages(self, x, stream=None):
         ds, pt = self.dev_status, x.get("page_table")
+        append = []
+        if self.cache is not None:
+            c, new = self.cache, x
+            append = [("append", lambda: c.append(new["q"], new["k"], new["v"], new["kI"], new["lengths"], self.T, pt,
+                                                  self.q_rot, stream, ds))]
+            x = dict(x, q=self.q_rot, k=c.k, v=c.v, kI=c.kI, k_scale=c.k_scale, v_scale=c.v_scale)
         if self.fused:
             select = [("indexer_topk", lambda: sa_indexer_topk_decode(
                 x["qI"], x["w"], x["kI"], pt, self.max_pages, self.pool_pages, 64, self.B, self.S, self.H_I,
@@ -185,19 +292,25 @@ class DecodePlan:
         else:
             select = [
                 ("indexer", lambda: self.index(x["qI"], x["w"], x["kI"], pt, self.max_pages, self.pool_pages,
-                                               64, self.B, 1, self.S, self.H_I, self.D_I, x["lengths"],
+                                               64, self.B, self.T, self.S, self.H_I, self.D_I, x["lengths"],
                                                self.scores, self.ld, ds, stream)),
-                ("topk", lambda: sa_topk_select(self.scores, self.ld, self.B, self.S, x["lengths"], None, 0,
+                ("topk", lambda: sa_topk_select(self.scores, self.ld, self.B * self.T, self.S, x["lengths"], None, 0,
                                                 self.K, self.topk, ds, stream))]
-        return select + [
-            ("attention", lambda: sa_sparse_attn_decode(
+        if self.kv_q8:
+            attention = ("attention", lambda: sa_sparse_attn_q8(
+                x["q"], x["k"], x["v"], x["k_scale"], x["v_scale"], self.scale_block, pt, self.max_pages,
+                self.pool_pages, 64, self.S_max, x["lengths"], self.topk, self.K, self.W, self.B, self.T, self.Hq,
+                self.d, self.scale, self.out, self.lse, ds, stream))
+        else:
+            attention = ("attention", lambda: sa_sparse_attn_decode(
                 x["q"], x["k"], x["v"], pt, self.max_pages, self.pool_pages, 64, self.S_max, x["lengths"],
                 self.topk, self.K, self.W, self.B, self.Hq, self.d, self.scale, self.out, self.lse,
-                self.workspace, self.ws_bytes, ds, stream)),
-        ]
+                self.workspace, self.ws_bytes, ds, stream))
+        return append + select + [attention]
 
-    def run(self, q, k_cache, v_cache, qI, w, kI, seq_lens, page_table=None, stream=None):
-        x = dict(q=q, k=k_cache, v=v_cache, qI=qI, w=w, kI=kI, lengths=seq_lens, page_table=page_table)
+    def run(self, q, k_cache, v_cache, qI, w, kI, seq_lens, page_table=None, stream=None, k_scale=None, v_scale=None):
+        x = dict(q=q, k=k_cache, v=v_cache, qI=qI, w=w, kI=kI, lengths=seq_lens, page_table=page_table,
+                 k_scale=k_scale, v_scale=v_scale)
         for _, fn in self.stages(x, stream):
             fn()
         return self.out
@@ -208,10 +321,14 @@ class DecodePlan:
         sa_sparse_attn_decode.  That is one kernel when a thread-block cluster
         of G = min(16, max(1, ceil((K+W)/128), ceil(Hq/8))) CTAs per sequence
         leaves each CTA at most 1024 keys (partials merged in distributed
-        shared memory), else a split-K kernel and a merge kernel."""
+        shared memory), else a split-K kernel and a merge kernel.  The 8-bit
+        cache's attention is always one kernel; a plan with a cache appends
+        in one more."""
+        if self.kv_q8:
+            return (1 if self.fused else 2) + 1 + (self.cache is not None)
         kw = self.K + self.W
         G = min(16, max(1, -(-kw // 128), -(-self.Hq // 8)))
-        return (1 if self.fused else 2) + (1 if -(-kw // G) <= 1024 else 2)
+        return (1 if self.fused else 2) + (1 if -(-kw // G) <= 1024 else 2) + (self.cache is not None)
 
 
 class HostPipeline:

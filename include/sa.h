@@ -391,6 +391,125 @@ sa_status sa_sparse_attn_decode_noalloc(const sa_bf16 *q,
                                         int *dev_status, sa_stream stream);
 
 /* ------------------------------------------------------------------------
+ * Filling the caches: append the keys and values of new tokens, rotated to
+ * their positions ("Sparse Attention", completesystemdesign, DSA list: 64-token
+ * KV pages; "Where Sparse Attention Is Actually Sparse": the indexer's keys
+ * take no position).  One launch covers everything that the next indexer,
+ * top-K and attention calls read.
+ *
+ *   A step brings up to T new tokens for each of B sequences.  Row r = b*T + t
+ *   is token t of sequence b; n_valid[r] is its position + 1 (the number of
+ *   cached tokens it sees once the step is appended, as sa_indexer_scores and
+ *   sa_sparse_attn_q8 take it), or 0 for a padding row, of which nothing is
+ *   read and nothing written.  With p = n_valid[r] - 1:
+ *     a_i = p * inv_freq[i], i < rot_dim / 2, and the pairs (i, i + rot_dim/2)
+ *     or, with interleaved != 0, (2i, 2i + 1) of every head turn by it:
+ *       x'_first = x_first cos a_i - x_second sin a_i
+ *       x'_second = x_second cos a_i + x_first sin a_i
+ *     dims >= rot_dim are copied;
+ *     q_out[r, h] = bf16(rot(q[r, h])),
+ *     k_cache[slot] = bf16(rot(k[r])), v_cache[slot] = v[r],
+ *     kI_cache[slot] = kI[r] (or its e4m3 conversion as sa_convert_e4m3 makes it)
+ *   where slot = page_table[b*max_pages + p/64]*64 + p%64, or b*S_max + p when
+ *   page_table == NULL.  The angle is reduced in fp64 (positions of any length
+ *   keep their accuracy); rotated values are fp32, rounded once.
+ *
+ *   q [B*T, ld_q] (Hq*d used), k, v [B*T, ld_k / ld_v] (d used), kI [B*T, ld_kI]
+ *   (D_I used): bf16 rows, 16-byte aligned, the strides ld_* in elements,
+ *   multiples of 8 (slices of one projection's output can be passed in place).
+ *   q_out [B*T, Hq, d] bf16; it may be q itself when ld_q == Hq*d.  q and q_out
+ *   may both be NULL (queries rotated elsewhere), so may kI and kI_cache (D_I
+ *   ignored).
+ *   inv_freq [rot_dim / 2] fp32 (NULL when rot_dim == 0); rot_dim a multiple of
+ *   16, 0 .. d.
+ *   Caches: contiguous [B, S_max, *], or pools [pool_pages, 64, *], 16-byte aligned.
+ *   kI_cache: bf16, or e4m3 when kI_e4m3 != 0; D_I in {32, 64, 128}.
+ *   The rows of one sequence must have distinct positions, and no page that
+ *   the step writes may belong to two sequences (which value stays is
+ *   unspecified otherwise).
+ *   Device errors: SA_DEV_INDEX for an n_valid outside [0, S_max] (paged: [0,
+ *   max_pages*64]) or a page id outside [0, pool_pages): the row's keys and
+ *   values are not written (a row out of range keeps its q_out too).
+ * ---------------------------------------------------------------------- */
+sa_status sa_cache_append(const sa_bf16 *q, int64_t ld_q, sa_bf16 *q_out,
+                          const sa_bf16 *k, int64_t ld_k, const sa_bf16 *v,
+                          int64_t ld_v, const sa_bf16 *kI, int64_t ld_kI,
+                          const int32_t *n_valid, const int32_t *page_table,
+                          int max_pages, int pool_pages, int page_size,
+                          int S_max, int B, int T, int Hq, int d, int D_I,
+                          const float *inv_freq, int rot_dim, int interleaved,
+                          sa_bf16 *k_cache, sa_bf16 *v_cache, void *kI_cache,
+                          int kI_e4m3, int *dev_status, sa_stream stream);
+
+/* The same append into a cache held in 8 bits.
+ *   k_cache, v_cache: e4m3 codes in the layouts above; k_scale, v_scale: one
+ *   fp32 scale for every scale_block consecutive tokens (a power of two, 1 ..
+ *   64; contiguous caches need S_max a multiple of it), [pool_pages, 64 /
+ *   scale_block] or [B, S_max / scale_block].  A cached value is code * scale.
+ *   For every block that receives tokens, with x its new (rotated, fp32) values:
+ *     need = the smallest 2^e, -64 <= e <= 64, with max |x| <= 448 * 2^e (over
+ *            finite x; 2^-64 for a block of zeros);
+ *     scale = need if the step's tokens begin the block (whatever it held is
+ *             replaced), else max(need, the block's old scale, taken into
+ *             [2^-64, 2^64]);
+ *     code = e4m3(x / scale), rounded to nearest even, beyond +-448 and
+ *            infinities saturated, NaN kept;
+ *     and if the scale grew, the codes of the block's earlier tokens become
+ *     e4m3(code * old / scale).
+ *   A power of two costs no precision (e4m3 is a floating format) and makes
+ *   that second rounding exact outside of e4m3's subnormals.  The slots behind
+ *   the step's last token are left as they are.
+ *   The valid rows of a sequence must be consecutive rows with consecutive
+ *   positions (padding only in front or behind): otherwise SA_DEV_ORDER, and
+ *   nothing of that sequence is written but its q_out rows. */
+sa_status sa_cache_append_q8(const sa_bf16 *q, int64_t ld_q, sa_bf16 *q_out,
+                             const sa_bf16 *k, int64_t ld_k, const sa_bf16 *v,
+                             int64_t ld_v, const sa_bf16 *kI, int64_t ld_kI,
+                             const int32_t *n_valid, const int32_t *page_table,
+                             int max_pages, int pool_pages, int page_size,
+                             int S_max, int B, int T, int Hq, int d, int D_I,
+                             const float *inv_freq, int rot_dim, int interleaved,
+                             sa_e4m3 *k_cache, sa_e4m3 *v_cache, float *k_scale,
+                             float *v_scale, int scale_block, void *kI_cache,
+                             int kI_e4m3, int *dev_status, sa_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Stage 3c -- sparse attention over an 8-bit cache: one new token or a chunk
+ * of T tokens a sequence, contiguous or paged
+ *
+ *   Row r = b*T + t sits at position p = n_valid[r] - 1 of sequence b.  Its key
+ *   set is, as in prefill and decode,
+ *     S(r) = {s in topk[r, :] : 0 <= s <= p - W} U {max(0, p-W+1) .. p}
+ *   and with the cached values k = code * k_scale[block], v = code * v_scale[block]
+ *   (as sa_cache_append_q8 writes them)
+ *     out[r,h,:] = sum_{s in S(r)} softmax_s(q[r,h,:] . k[s,:] * scale) v[s,:]
+ *     lse[r,h] = log(sum_s exp(q.k*scale)), if lse != NULL.
+ *   A row whose set is empty (n_valid = 0: padding; or W = 0 and no valid
+ *   top-K entry) gives out 0 and lse -infinity.
+ *   q [B*T, Hq, d] bf16, topk [B*T, K] ascending, -1 padded (as sa_topk_select
+ *   writes it with the same n_valid), out [B*T, Hq, d] bf16, lse [B*T, Hq]
+ *   fp32; q, out and the caches 16-byte aligned.  Scales are read as numbers in
+ *   [2^-64, 2^64] (others are taken to the nearer end).
+ *   Softmax and accumulation are fp32.  No workspace: the rows of small steps
+ *   are split over thread-block clusters and joined in shared memory.
+ *   Errors: K + W = 0 is SA_ERR_INVALID_ARG; SA_ERR_UNSUPPORTED if B * S_max
+ *   or pool_pages * 64 exceeds INT32_MAX rows, or K + W > 524288; device
+ *   SA_DEV_INDEX for an n_valid outside the cache (that row is treated as
+ *   empty), a top-K entry > p or a page id outside the pool (that key is
+ *   skipped); SA_DEV_ORDER for a row that is not strictly ascending;
+ *   SA_DEV_TIMEOUT.
+ * ---------------------------------------------------------------------- */
+sa_status sa_sparse_attn_q8(const sa_bf16 *q, const sa_e4m3 *k_cache,
+                            const sa_e4m3 *v_cache, const float *k_scale,
+                            const float *v_scale, int scale_block,
+                            const int32_t *page_table, int max_pages,
+                            int pool_pages, int page_size, int S_max,
+                            const int32_t *n_valid, const int32_t *topk, int K,
+                            int W, int B, int T, int Hq, int d, float scale,
+                            sa_bf16 *out, float *lse, int *dev_status,
+                            sa_stream stream);
+
+/* ------------------------------------------------------------------------
  * Two-stage selection helpers ("What Fine-Grained Means": a coarse block pass
  * picks candidate regions cheaply, a fine pass picks top-K tokens inside
  * them; section 2 "Learned Block Routing": blocks are mean-pooled over
