@@ -119,10 +119,11 @@ def attention(q, kc, vc, ks, vs, sb, pt, S_max, nv, topk, W, T, scale):
         # fp32 scores: 2^-22 of their products' magnitudes; exp2 2^-22; sums of n terms n 2^-24
         mag = ((qr.abs() @ kcode.abs().T) * kscale * abs(scale)).max()
         rel = float(dx + mag * 2.0 ** -22) * 2 + 2.0 ** -18 + len(keys) * 2.0 ** -24
-        # P in two e4m3 parts: 2^-8 of its value (half a step of the rest), and among
-        # the subnormals 2^-10 for either part, where the largest P is at least 64
+        # P in fp16 (2^-12 of its value) and two e4m3 parts, the second times 16: 2^-8 of
+        # its value (half a step of the rest), and 2^-14 among the second part's
+        # subnormals, where the largest P is at least 2
         aw = wv @ vcode.abs()
         floor = wv.max(-1).values[:, None] * vcode.abs().sum(0)[None] * 2.0 ** -15
-        tol_o[r] = 2.0 ** -8 * out[r].abs() + (2.0 ** -8 + rel) * aw + floor
+        tol_o[r] = 2.0 ** -8 * out[r].abs() + (2.0 ** -8 + 2.0 ** -12 + rel) * aw + floor
         tol_l[r] = rel + 2.0 ** -22 * z.abs()
     return out, lse, tol_o, tol_l, sizes
