@@ -47,7 +47,6 @@ namespace sa {
 namespace {
 
 constexpr int kTile = 128;                  // keys per tile (MMA M)
-constexpr int kHG = 16;                     // heads a softmax thread handles
 constexpr float kTop = 1.f, kRaise = 8.75f; // log2 of the largest P after a raise, and before the next
 constexpr float kLowest = -1e30f;           // running maximum of a row that has met no key yet
 constexpr int kSmemSm = 233472;             // shared memory of an SM, 1 KB of it reserved per CTA
@@ -63,7 +62,8 @@ template <int D_, int HQP_>
 struct Cfg {
     static constexpr int D = D_, HQP = HQP_;
     static constexpr int N2 = 2 * HQP;                    // MMA N: hi and lo columns
-    static constexpr int NG = HQP / kHG;                  // softmax groups of 128 threads
+    static constexpr int HG = HQP == 16 ? 16 : 32;        // heads a softmax thread handles
+    static constexpr int NG = HQP / HG;                   // softmax groups of 128 threads
     static constexpr int kThreads = 128 * NG;
     static constexpr int kKV = kTile * D, kQ = N2 * D, kP = kTile * N2;
     static constexpr int kOffK = 0;
@@ -73,7 +73,7 @@ struct Cfg {
     static constexpr int kOffRows = kOffP + kP;                       // [3][128] cache rows of a tile's keys
     static constexpr int kOffSc = kOffRows + 3 * kTile * 4;           // [2][3][128] score factor, log2 vs, 1 / vs
     static constexpr int kOffMax = kOffSc + 2 * 3 * kTile * 4;           // [4][HQP] maxima or sums of the quads
-    static constexpr int kOffNegM = kOffMax + 4 * HQP * 4;            // [warp][16] minus the running maxima
+    static constexpr int kOffNegM = kOffMax + 4 * HQP * 4;            // [warp][HG] minus the running maxima
     static constexpr int kOffEpi = kOffNegM + 4 * HQP * 4;            // m, l [2][HQP]
     static constexpr int kOffMerge = kOffEpi + 2 * HQP * 4;           // [2][HQP + 16] m, l of every CTA (clusters)
     static constexpr int kOffMisc = kOffMerge + 2 * (HQP + 16) * 4;
@@ -199,7 +199,7 @@ __device__ __forceinline__ uint64_t desc_v(uint32_t addr) {
 template <int D, int HQP>
 __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) attn_q8_kernel(Params P) {
     using C = Cfg<D, HQP>;
-    constexpr int N2 = C::N2, NT = C::kThreads;
+    constexpr int N2 = C::N2, NT = C::kThreads, HG = C::HG;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     int32_t *rows = reinterpret_cast<int32_t *>(sm + C::kOffRows);
@@ -220,12 +220,17 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     // thread) and its top-K.
     const int nv = __ldg(A.n_valid + r);
     constexpr int CPH = D / 16;   // 16-dim chunks of a head
-    uint4 qa = make_uint4(0, 0, 0, 0), qb = qa;
-    const bool has_q = tid < A.Hq * CPH;
-    if (has_q) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (int64_t)r * A.Hq * D) + 2 * tid;
-        qa = __ldg(src);
-        qb = __ldg(src + 1);
+    constexpr int NQ = (HQP * CPH + NT - 1) / NT;   // chunks a thread
+    uint4 qv[2 * NQ];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+        const int c = tid + i * NT;
+        qv[2 * i] = qv[2 * i + 1] = make_uint4(0, 0, 0, 0);
+        if (c < A.Hq * CPH) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (int64_t)r * A.Hq * D) + 2 * c;
+            qv[2 * i] = __ldg(src);
+            qv[2 * i + 1] = __ldg(src + 1);
+        }
     }
     if (tid == 0) {
         mbar_init(bar, 1);
@@ -233,11 +238,6 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         *s_first = (unsigned)A.K;
         *s_qmax = 0;
         fence_mbar_init();
-    }
-    // heads >= Hq of both parts are zeros
-    for (int i = A.Hq * CPH + tid; i < HQP * CPH; i += NT) {
-        *reinterpret_cast<uint4 *>(sm + C::kOffQ + sw<D>(i / CPH, i % CPH)) = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4 *>(sm + C::kOffQ + sw<D>(HQP + i / CPH, i % CPH)) = make_uint4(0, 0, 0, 0);
     }
     if (warp == 0) {
         tmem_alloc(tmem_slot, C::kTmemCols);
@@ -281,11 +281,14 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         if (rank == 0 && bad_ord) report(A.dev_status, SA_DEV_ORDER);
         first_out = (int)__reduce_min_sync(0xffffffffu, (unsigned)first_out);
         uint32_t mx = 0;   // largest finite |q|
-        const uint32_t w[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint32_t t = w[k] & 0x7FFF7FFFu;
-            mx = __vmaxu2(mx, t & __vcmpltu2(t, 0x7F807F80u));
+        for (int i = 0; i < 2 * NQ; ++i) {
+            const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t t = w[k] & 0x7FFF7FFFu;
+                mx = __vmaxu2(mx, t & __vcmpltu2(t, 0x7F807F80u));
+            }
         }
         mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
         if (lane == 0) {
@@ -306,13 +309,13 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             for (int i = tid; i < A.Hq; i += NT) A.lse[(int64_t)r * A.Hq + i] = -CUDART_INF_F;
     }
 
-    const int quad = warp & 3, hg = warp >> 2, h0 = hg * kHG;
+    const int quad = warp & 3, hg = warp >> 2, h0 = hg * HG;
     const int key = quad * 32 + lane;                     // TMEM lane: key (S^T) or head dim (O^T)
     const uint32_t lane_t = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)h0;
-    f2 l[kHG / 2];
+    f2 l[HG / 2];
 #pragma unroll
-    for (int i = 0; i < kHG / 2; ++i) l[i] = 0;
-    float *negm = reinterpret_cast<float *>(sm + C::kOffNegM) + warp * kHG;   // this warp's copy
+    for (int i = 0; i < HG / 2; ++i) l[i] = 0;
+    float *negm = reinterpret_cast<float *>(sm + C::kOffNegM) + warp * HG;   // this warp's copy
 
     if (i0 < i1) {
         // the largest value's power of two, so that it lies in (224, 448]; at least 2^-120
@@ -374,8 +377,13 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         };
         gather(i0, A.k, C::kOffK);
         gather(i0, A.v, C::kOffV);
-        if (has_q) {   // both parts of this thread's 16 dims, while the copies fly
-            const uint32_t w[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
+        // both parts of this thread's chunks of Q, while the copies fly (heads >= Hq are zeros)
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            const int c = tid + i * NT;
+            if (c >= HQP * CPH) break;
+            const uint4 q0 = qv[2 * i], q1 = qv[2 * i + 1];
+            const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -389,10 +397,10 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 hi[k / 2] = k & 1 ? hi[k / 2] | h << 16 : h;
                 lo[k / 2] = k & 1 ? lo[k / 2] | e << 16 : e;
             }
-            *reinterpret_cast<uint4 *>(sm + C::kOffQ + sw<D>(tid / CPH, tid % CPH)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(sm + C::kOffQ + sw<D>(HQP + tid / CPH, tid % CPH)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4 *>(sm + C::kOffQ + sw<D>(c / CPH, c % CPH)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(sm + C::kOffQ + sw<D>(HQP + c / CPH, c % CPH)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
-        if (lane < kHG) negm[lane] = 0.f;
+        if (lane < HG) negm[lane] = 0.f;
         cp_async_wait_all();
         fence_async_smem();
         __syncthreads();
@@ -439,11 +447,11 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             const float *kf = sc + (t & 1) * 3 * kTile + key;
             const float lv = kf[kTile];
             const f2 c2 = pk(kf[0], kf[0]), lv2 = pk(lv, lv), iv2 = pk(kf[2 * kTile], kf[2 * kTile]);
-            f2 e[kHG / 2];
+            f2 e[HG / 2];
             float emax = -CUDART_INF_F;
             const ulonglong2 *nm = reinterpret_cast<const ulonglong2 *>(negm);
 #pragma unroll
-            for (int c = 0; c < kHG; c += 8) {
+            for (int c = 0; c < HG; c += 8) {
                 uint32_t u[8], v[8];
                 tmem_ld_x8(lane_t + (uint32_t)c, u);
                 tmem_ld_x8(lane_t + (uint32_t)(HQP + c), v);
@@ -461,23 +469,23 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             if (bar_or(1 + 2 * hg, 128, fresh || emax > kRaise)) {
                 float *gmax = reinterpret_cast<float *>(sm + C::kOffMax) + h0 * 4;   // [quad][16]
 #pragma unroll
-                for (int i = 0; i < kHG / 2; ++i) {
+                for (int i = 0; i < HG / 2; ++i) {
                     const float2 f = up(e[i]);
                     const float x = redux_max(f.x), y = redux_max(f.y);
-                    if (lane == 0) *reinterpret_cast<float2 *>(gmax + quad * kHG + 2 * i) = make_float2(x, y);
+                    if (lane == 0) *reinterpret_cast<float2 *>(gmax + quad * HG + 2 * i) = make_float2(x, y);
                 }
                 bar_sync_n(2 + 2 * hg, 128);
                 // a head a lane: how far its maximum goes up, and what that makes of the sums
                 float up_by = 0.f;
-                if (lane < kHG) {
-                    const float tm = fmaxf(fmaxf(gmax[lane], gmax[kHG + lane]), fmaxf(gmax[2 * kHG + lane], gmax[3 * kHG + lane]));
+                if (lane < HG) {
+                    const float tm = fmaxf(fmaxf(gmax[lane], gmax[HG + lane]), fmaxf(gmax[2 * HG + lane], gmax[3 * HG + lane]));
                     if (tm > (fresh ? kLowest : kRaise)) up_by = tm - kTop;
                 }
                 const float f = ex2f(-up_by);
                 const bool resc = !fresh && __any_sync(0xffffffffu, up_by != 0.f);
-                if (lane < kHG) negm[lane] -= up_by;
+                if (lane < HG) negm[lane] -= up_by;
 #pragma unroll
-                for (int c = 0; c < kHG; c += 8) {
+                for (int c = 0; c < HG; c += 8) {
                     float fc[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) fc[k] = __shfl_sync(0xffffffffu, f, c + k);
@@ -506,20 +514,23 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             // P^T as an MN-major operand without swizzle: 16-byte rows of 16 heads, the
             // rows of 8 keys 16 bytes apart, the head chunks of a key group 128 bytes
             // apart (first all high parts, then the low ones), key groups N2 * 8 bytes apart
-            uint32_t hi[4], lo[4];
+            uint8_t *pbuf = sm + C::kOffP + (key >> 3) * (N2 * 8) + (key & 7) * 16 + (h0 / 16) * 128;
 #pragma unroll
-            for (int i = 0; i < kHG / 2; ++i) {
-                const float2 f = up(e[i]);
-                const float p0 = ex2f(f.x), p1 = ex2f(f.y);
-                l[i] = fma2(pk(p0, p1), iv2, l[i]);
-                const uint32_t p16 = f16x2(p0, p1), h = e4m3x2_of_f16(p16);
-                const uint32_t d = e4m3x2_of_f16(hmul2(hsub2(p16, f16x2_of_e4m3(h)), 0x4C004C00u));   // the rest times 16
-                hi[i / 2] = i & 1 ? hi[i / 2] | h << 16 : h;
-                lo[i / 2] = i & 1 ? lo[i / 2] | d << 16 : d;
+            for (int c = 0; c < HG / 16; ++c) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 f = up(e[8 * c + i]);
+                    const float p0 = ex2f(f.x), p1 = ex2f(f.y);
+                    l[8 * c + i] = fma2(pk(p0, p1), iv2, l[8 * c + i]);
+                    const uint32_t p16 = f16x2(p0, p1), h = e4m3x2_of_f16(p16);
+                    const uint32_t d = e4m3x2_of_f16(hmul2(hsub2(p16, f16x2_of_e4m3(h)), 0x4C004C00u));   // the rest times 16
+                    hi[i / 2] = i & 1 ? hi[i / 2] | h << 16 : h;
+                    lo[i / 2] = i & 1 ? lo[i / 2] | d << 16 : d;
+                }
+                *reinterpret_cast<uint4 *>(pbuf + c * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(pbuf + (HQP / 16 + c) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
-            uint8_t *pbuf = sm + C::kOffP + (key >> 3) * (N2 * 8) + (key & 7) * 16 + hg * 128;
-            *reinterpret_cast<uint4 *>(pbuf) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(pbuf + (HQP / 16) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             if (tid < kTile && t + 1 < i1) {
                 put_scale(t + 1, row1, ks1, vs1);
                 row1 = put_row(t + 2, pos2, pg2);
@@ -547,18 +558,18 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         // ------------------------------------------------------------ the row's sums
         float *gsum = reinterpret_cast<float *>(sm + C::kOffMax) + h0 * 4;
 #pragma unroll
-        for (int i = 0; i < kHG / 2; ++i) {
+        for (int i = 0; i < HG / 2; ++i) {
             float2 v = up(l[i]);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
                 v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
                 v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
             }
-            if (lane == 0) *reinterpret_cast<float2 *>(gsum + quad * kHG + 2 * i) = v;
+            if (lane == 0) *reinterpret_cast<float2 *>(gsum + quad * HG + 2 * i) = v;
         }
         bar_sync_n(2 + 2 * hg, 128);
-        if (quad == 0 && lane < kHG) {
-            epi_l[h0 + lane] = (gsum[lane] + gsum[kHG + lane]) + (gsum[2 * kHG + lane] + gsum[3 * kHG + lane]);
+        if (quad == 0 && lane < HG) {
+            epi_l[h0 + lane] = (gsum[lane] + gsum[HG + lane]) + (gsum[2 * HG + lane] + gsum[3 * HG + lane]);
             epi_m[h0 + lane] = -negm[lane];
         }
         bar_sync_n(2 + 2 * hg, 128);
@@ -567,7 +578,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         float *part = reinterpret_cast<float *>(sm + C::kOffK);
         uint16_t *orow = A.out + (int64_t)r * A.Hq * D;
 #pragma unroll
-        for (int c = 0; c < kHG; c += 8) {
+        for (int c = 0; c < HG; c += 8) {
             uint32_t u[8], v[8];
             tmem_ld_x8(lane_t + (uint32_t)(N2 + c), u);
             tmem_ld_x8(lane_t + (uint32_t)(N2 + HQP + c), v);
@@ -587,7 +598,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 }
             }
         }
-        if (P.G == 1 && A.lse && quad == 0 && lane < kHG && h0 + lane < A.Hq) {
+        if (P.G == 1 && A.lse && quad == 0 && lane < HG && h0 + lane < A.Hq) {
             const float L = epi_l[h0 + lane];
             A.lse[(int64_t)r * A.Hq + h0 + lane] =
                 L == 0.f ? -CUDART_INF_F : (epi_m[h0 + lane] + log2f(L)) * 0.69314718055994531f;
