@@ -64,16 +64,16 @@ struct Cfg {
     static constexpr int N2 = 2 * HQP;                    // MMA N: hi and lo columns
     static constexpr int HG = HQP == 16 ? 16 : 32;        // heads a softmax thread handles
     static constexpr int NG = HQP / HG;                   // softmax groups of 128 threads
-    static constexpr int kThreads = 128 * NG;
+    static constexpr int kThreads = 128 + 128 * NG;       // loader warps, softmax warps
     static constexpr int kKV = kTile * D, kQ = N2 * D, kP = kTile * N2;
     static constexpr int kOffK = 0;
     static constexpr int kOffV = kOffK + kKV;
     static constexpr int kOffQ = kOffV + kKV;
     static constexpr int kOffP = kOffQ + kQ;
-    static constexpr int kOffRows = kOffP + kP;                       // [3][128] cache rows of a tile's keys
-    static constexpr int kOffSc = kOffRows + 3 * kTile * 4;           // [2][3][128] score factor, log2 vs, 1 / vs
+    static constexpr int kOffRows = kOffP + kP;                       // [2][128] cache rows of a tile's keys
+    static constexpr int kOffSc = kOffRows + 2 * kTile * 4;           // [2][3][128] score factor, log2 vs, 1 / vs
     static constexpr int kOffMax = kOffSc + 2 * 3 * kTile * 4;           // [4][HQP] maxima or sums of the quads
-    static constexpr int kOffNegM = kOffMax + 4 * HQP * 4;            // [warp][HG] minus the running maxima
+    static constexpr int kOffNegM = kOffMax + 4 * HQP * 4;            // [softmax warp][HG] minus the running maxima
     static constexpr int kOffEpi = kOffNegM + 4 * HQP * 4;            // m, l [2][HQP]
     static constexpr int kOffMerge = kOffEpi + 2 * HQP * 4;           // [2][HQP + 16] m, l of every CTA (clusters)
     static constexpr int kOffMisc = kOffMerge + 2 * (HQP + 16) * 4;
@@ -83,7 +83,9 @@ struct Cfg {
     // whatever shares an SM must fit its 512 columns: shared memory in proportion.
     static constexpr int kLeast = (int)(kTmemCols * (kSmemSm / 512)) - 1024;
     static constexpr int kSmem = kUsed > kLeast ? kUsed : kLeast;
-    static constexpr int kPerSm = kSmemSm / (kSmem + 1024);
+    // CTAs an SM: two to four by their registers (80 a thread, 64 with 16 heads)
+    static constexpr int kByRegs = HQP == 16 ? 4 : (HQP == 32 ? 3 : 2);
+    static constexpr int kPerSm = kSmemSm / (kSmem + 1024) < kByRegs ? kSmemSm / (kSmem + 1024) : kByRegs;
     static_assert(2 * kKV >= HQP * D * 4, "the partial O of a cluster's CTA lies in the K and V tiles");
 };
 
@@ -113,6 +115,11 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     f2 r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{ .reg .pred p; .reg .b32 d; elect.sync d|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
 }
 __device__ __forceinline__ float redux_max(float x) {   // NaN counts as absent
     float r;
@@ -206,12 +213,13 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     float *sc = reinterpret_cast<float *>(sm + C::kOffSc);
     float *epi_m = reinterpret_cast<float *>(sm + C::kOffEpi), *epi_l = epi_m + HQP;
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + C::kOffMisc);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 1);
+    uint64_t *bar_s = bar, *bar_pv = bar + 1;   // S(t), P V(t) done
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 2);
     int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
     unsigned *s_first = reinterpret_cast<unsigned *>(tmem_slot + 2), *s_qmax = s_first + 1;
 
     const AttnQ8Args &A = P.a;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int rank = P.G > 1 ? (int)cluster_rank() : 0;
     const int r = (int)blockIdx.x / P.G, b = r / A.T;
 
@@ -233,7 +241,8 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         }
     }
     if (tid == 0) {
-        mbar_init(bar, 1);
+        mbar_init(bar_s, 1);
+        mbar_init(bar_pv, 1);
         *abort_flag = 0;
         *s_first = (unsigned)A.K;
         *s_qmax = 0;
@@ -246,7 +255,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;   // S (N2 columns), O (N2 columns)
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);   // S (N2 columns), O (N2 columns)
 
     int p = nv - 1;
     if (nv < 0 || nv > A.S_max) {
@@ -309,13 +318,12 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             for (int i = tid; i < A.Hq; i += NT) A.lse[(int64_t)r * A.Hq + i] = -CUDART_INF_F;
     }
 
-    const int quad = warp & 3, hg = warp >> 2, h0 = hg * HG;
+    const bool loader = warp < 4;
+    // softmax warps: TMEM lane quadrant, group, first head
+    const int quad = warp & 3, hg = loader ? 0 : (warp >> 2) - 1, h0 = hg * HG;
     const int key = quad * 32 + lane;                     // TMEM lane: key (S^T) or head dim (O^T)
     const uint32_t lane_t = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)h0;
-    f2 l[HG / 2];
-#pragma unroll
-    for (int i = 0; i < HG / 2; ++i) l[i] = 0;
-    float *negm = reinterpret_cast<float *>(sm + C::kOffNegM) + warp * HG;   // this warp's copy
+    float *negm = reinterpret_cast<float *>(sm + C::kOffNegM) + (hg * 4 + quad) * HG;   // this warp's copy
 
     if (i0 < i1) {
         // the largest value's power of two, so that it lies in (224, 448]; at least 2^-120
@@ -325,7 +333,8 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         const float down = __int_as_float((127 - e2) << 23);
         const float factor = __int_as_float((e2 + 127) << 23) * P.scale_log2;
 
-        // lookups of threads 0 .. 127, one key each: position (-1: none), page, cache row, scales
+        constexpr int RPT = 128 / CPH, NIT = kTile / RPT;   // rows that the loader threads copy at once, turns
+        // lookups of the loader threads, one key each: position (-1: none), page, cache row, scales
         const int32_t *pt = A.page_table ? A.page_table + (int64_t)b * A.max_pages : nullptr;
         auto position = [&](int t) {
             const int kk = t * kTile + tid;
@@ -339,7 +348,8 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 else if (page >= 0 && page < A.pool_pages) row = page * 64 + (pos & 63);
                 else report(A.dev_status, SA_DEV_INDEX);
             }
-            rows[(t % 3) * kTile + tid] = row;
+            // in the order the copies take them: key 16 i + c is number i of the c-th row of threads
+            rows[(t & 1) * kTile + (tid % RPT) * NIT + tid / RPT] = row;
             return row;
         };
         auto put_scale = [&](int t, int row, float ks, float vs) {
@@ -350,7 +360,8 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             o[2 * kTile] = row >= 0 ? __frcp_rn(vs) : 0.f;
         };
         int pos2 = -1, row1 = -1;   // the key of tile t + 2, the cache row of tile t + 1's
-        if (tid < kTile) {
+        int ids[NIT];               // the rows that this thread copies of tile t
+        if (loader) {
             const int pos0 = position(i0), pos1 = position(i0 + 1);
             const int pg0 = page_of(pos0), pg1 = page_of(pos1);
             pos2 = position(i0 + 2);
@@ -366,17 +377,36 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         __syncthreads();
 
         // copies of a tile's rows, D / 16 threads a row
-        auto gather = [&](int t, const uint8_t *src, int off) {
-            constexpr int RPT = NT / CPH;   // rows at once
-            const int ch = tid % CPH, row0 = tid / CPH;
+        auto load_ids = [&](int t, int (&ids)[NIT]) {
 #pragma unroll
-            for (int i = 0; i < kTile / RPT; ++i) {
-                const int k = row0 + i * RPT, row = rows[(t % 3) * kTile + k];
-                cp_async16_or_zero(sm + off + sw<D>(k, ch), src + (int64_t)max(row, 0) * D + ch * 16, row >= 0);
+            for (int q = 0; q < NIT / 4; ++q)
+                reinterpret_cast<int4 *>(ids)[q] = reinterpret_cast<const int4 *>(rows + (t & 1) * kTile + (tid / CPH) * NIT)[q];
+        };
+        auto gather = [&](const uint8_t *src, int off, const int (&ids)[NIT], bool full) {
+            const uint8_t *from = src + (tid % CPH) * 16;
+            uint8_t *to = sm + off + sw<D>(tid / CPH, tid % CPH);   // RPT is a multiple of 8: one swizzle for all rows
+            if (full) {
+#pragma unroll
+                for (int i = 0; i < NIT; ++i) cp_async16(to + i * RPT * D, from + (int64_t)ids[i] * D);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NIT; ++i)
+                    cp_async16_or_zero(to + i * RPT * D, from + (int64_t)max(ids[i], 0) * D, ids[i] >= 0);
             }
         };
-        gather(i0, A.k, C::kOffK);
-        gather(i0, A.v, C::kOffV);
+        bool full0 = false;   // tile t has no slot without a key
+        auto all_keys = [&](const int (&ids)[NIT]) {
+            int a = ids[0];
+#pragma unroll
+            for (int i = 1; i < NIT; ++i) a = min(a, ids[i]);
+            return __all_sync(0xffffffffu, a >= 0) != 0;
+        };
+        if (loader) {
+            load_ids(i0, ids);
+            full0 = all_keys(ids);
+            gather(A.k, C::kOffK, ids, full0);
+            gather(A.v, C::kOffV, ids, full0);
+        }
         // both parts of this thread's chunks of Q, while the copies fly (heads >= Hq are zeros)
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
@@ -400,7 +430,6 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             *reinterpret_cast<uint4 *>(sm + C::kOffQ + sw<D>(c / CPH, c % CPH)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4 *>(sm + C::kOffQ + sw<D>(HQP + c / CPH, c % CPH)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
-        if (lane < HG) negm[lane] = 0.f;
         cp_async_wait_all();
         fence_async_smem();
         __syncthreads();
@@ -422,186 +451,223 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 tc_mma_f8(tmem + N2, vd + (uint64_t)((kk * 32 * D) >> 4), pd + (uint64_t)((kk * 4 * N2 * 8) >> 4), idesc,
                           (first && kk == 0) ? 0u : 1u);
         };
-        if (tid == 0) {
+        if (warp == 0 && elect_one()) {
             issue_s();
-            tc_commit(bar);
+            tc_commit(bar_s);
         }
         __syncwarp();
-        bool ok = true, fresh = true;   // fresh: no key yet, m is still 0
-        for (int t = i0; t < i1; ++t) {
-            ok = gwait(bar, (uint32_t)(t - i0) & 1u, abort_flag);   // S(t), P V(t - 1)
-            tc_fence_after();
-            if (t > i0) gather(t, A.v, C::kOffV);
-            if (t + 1 < i1) gather(t + 1, A.k, C::kOffK);
-            // lookups ahead: the page of tile t + 2's key, the scales of tile t + 1's
-            int pg2 = 0;
-            float ks1 = 0.f, vs1 = 0.f;
-            if (tid < kTile) {
-                pg2 = page_of(pos2);
+        bool ok = true;
+        if (loader) {
+            // ------------------------------------------------------------ loader warps
+            for (int t = i0; t < i1; ++t) {
+                // lookups ahead: the page of tile t + 2's key, the scales of tile t + 1's
+                const int pg2 = page_of(pos2);
+                float ks1 = 0.f, vs1 = 0.f;
                 if (row1 >= 0) {
                     ks1 = __ldg(A.k_scale + (row1 >> P.sb_shift));
                     vs1 = __ldg(A.v_scale + (row1 >> P.sb_shift));
                 }
+                const int pos3 = position(t + 3);
+                ok = gwait(bar_s, (uint32_t)(t - i0) & 1u, abort_flag);   // the K tile is free
+                int ids1[NIT];
+                bool full1 = false;
+                if (t + 1 < i1) {
+                    load_ids(t + 1, ids1);
+                    full1 = all_keys(ids1);
+                    gather(A.k, C::kOffK, ids1, full1);
+                }
+                if (t > i0) {
+                    ok = ok && gwait(bar_pv, (uint32_t)(t - i0 - 1) & 1u, abort_flag);   // the V tile is free
+                    gather(A.v, C::kOffV, ids, full0);
+                }
+                if (t + 1 < i1) {
+                    put_scale(t + 1, row1, ks1, vs1);
+                    row1 = put_row(t + 2, pos2, pg2);
+                    pos2 = pos3;
+                    full0 = full1;
+#pragma unroll
+                    for (int i = 0; i < NIT; ++i) ids[i] = ids1[i];
+                }
+                cp_async_wait_all();
+                fence_async_smem();
+                if (__syncthreads_or(!ok)) {   // a wait ran out
+                    ok = false;
+                    break;
+                }
+                if (warp == 0 && elect_one()) {
+                    tc_fence_after();
+                    if (t + 1 < i1) {   // first: the softmax of t + 1 starts while P V(t) runs
+                        issue_s();
+                        tc_commit(bar_s);
+                    }
+                    issue_pv(t == i0);
+                    tc_commit(bar_pv);
+                }
+                __syncwarp();
             }
-            // e: log2 of P
-            const float *kf = sc + (t & 1) * 3 * kTile + key;
-            const float lv = kf[kTile];
-            const f2 c2 = pk(kf[0], kf[0]), lv2 = pk(lv, lv), iv2 = pk(kf[2 * kTile], kf[2 * kTile]);
-            f2 e[HG / 2];
-            float emax = -CUDART_INF_F;
-            const ulonglong2 *nm = reinterpret_cast<const ulonglong2 *>(negm);
+            if (ok) ok = gwait(bar_pv, (uint32_t)(i1 - i0 - 1) & 1u, abort_flag);
+            if (!ok && tid == 0) report(A.dev_status, SA_DEV_TIMEOUT);
+        } else {
+            // ------------------------------------------------------------ softmax warps
+            f2 l[HG / 2];
+#pragma unroll
+            for (int i = 0; i < HG / 2; ++i) l[i] = 0;
+            float *gmax = reinterpret_cast<float *>(sm + C::kOffMax) + h0 * 4;   // [quad][HG]
+            uint8_t *pbuf = sm + C::kOffP + (key >> 3) * (N2 * 8) + (key & 7) * 16 + (h0 / 16) * 128;
+            float m = kLowest;   // a head a lane: its running maximum
+            if (lane < HG) negm[lane] = -m;
+            for (int t = i0; t < i1; ++t) {
+                ok = gwait(bar_s, (uint32_t)(t - i0) & 1u, abort_flag);
+                tc_fence_after();
+                const float *kf = sc + (t & 1) * 3 * kTile + key;
+                const f2 c2 = pk(kf[0], kf[0]), lv2 = pk(kf[kTile], kf[kTile]), iv2 = pk(kf[2 * kTile], kf[2 * kTile]);
+                // Scores (with the value's scale, in log2) of 8 heads.  They are read from TMEM
+                // for the maxima and again for P: 32 registers less than keeping them.
+                auto scores = [&](int c, f2 (&x)[4]) {
+                    uint32_t u[8], v[8];
+                    tmem_ld_x8(lane_t + (uint32_t)c, u);
+                    tmem_ld_x8(lane_t + (uint32_t)(HQP + c), v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = add2(pku(u[2 * i], u[2 * i + 1]), pku(v[2 * i], v[2 * i + 1]));
+                };
+                // the tile's maximum of every head, over this warp's keys and then the group's
+                float tm = -CUDART_INF_F;
+#pragma unroll
+                for (int c = 0; c < HG; c += 8) {
+                    f2 x[4];
+                    scores(c, x);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = up(fma2(x[i], c2, lv2));
+                        const float a = redux_max(f.x), b = redux_max(f.y);
+                        if (lane == c + 2 * i) tm = a;
+                        if (lane == c + 2 * i + 1) tm = b;
+                    }
+                }
+                if (lane < HG) gmax[quad * HG + lane] = tm;
+                bar_sync_n(2 + hg, 128);
+                if (lane < HG) tm = fmaxf(fmaxf(gmax[lane], gmax[HG + lane]), fmaxf(gmax[2 * HG + lane], gmax[3 * HG + lane]));
+                if (t > i0) ok = ok && gwait(bar_pv, (uint32_t)(t - i0 - 1) & 1u, abort_flag);   // O and the P tile are free
+                tc_fence_after();
+                const bool raise = tm > m + kRaise;
+                const uint32_t raised = __ballot_sync(0xffffffffu, raise);
+                if (raised) {
+                    float f = 1.f;
+                    if (raise) {
+                        f = ex2f(m - (tm - kTop));
+                        m = tm - kTop;
+                        negm[lane] = -m;
+                    }
+                    if (t > i0) {   // what the row's earlier tiles made of these heads shrinks
+#pragma unroll
+                        for (int c = 0; c < HG; c += 8) {
+                            if (!((raised >> c) & 0xFFu)) continue;
+                            float fc[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) fc[k] = __shfl_sync(0xffffffffu, f, c + k);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) l[c / 2 + i] = fma2(l[c / 2 + i], pk(fc[2 * i], fc[2 * i + 1]), 0);
+#pragma unroll
+                            for (int part = 0; part < 2; ++part) {
+                                uint32_t o[8];
+                                tmem_ld_x8(lane_t + (uint32_t)(N2 + part * HQP + c), o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fc[k]);
+                                tmem_st8(lane_t + (uint32_t)(N2 + part * HQP + c), o);
+                            }
+                        }
+                        tmem_st_wait_all();
+                    }
+                    __syncwarp();
+                }
+                // P^T as an MN-major operand without swizzle: 16-byte rows of 16 heads, the
+                // rows of 8 keys 16 bytes apart, the head chunks of a key group 128 bytes
+                // apart (first all high parts, then the low ones), key groups N2 * 8 bytes apart
+#pragma unroll
+                for (int c = 0; c < HG; c += 16) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        f2 x[4];
+                        scores(c + 8 * half, x);
+                        const ulonglong2 n0 = reinterpret_cast<const ulonglong2 *>(negm + c + 8 * half)[0];
+                        const ulonglong2 n1 = reinterpret_cast<const ulonglong2 *>(negm + c + 8 * half)[1];
+                        const f2 nm[4] = {n0.x, n0.y, n1.x, n1.y};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 f = up(fma2(x[i], c2, add2(lv2, nm[i])));   // log2 of P
+                            const float p0 = ex2f(f.x), p1 = ex2f(f.y);
+                            f2 &sum = l[c / 2 + 4 * half + i];
+                            sum = fma2(pk(p0, p1), iv2, sum);
+                            const uint32_t p16 = f16x2(p0, p1), h = e4m3x2_of_f16(p16);
+                            const uint32_t d = e4m3x2_of_f16(hmul2(hsub2(p16, f16x2_of_e4m3(h)), 0x4C004C00u));   // the rest times 16
+                            uint32_t &hw = hi[2 * half + i / 2], &lw = lo[2 * half + i / 2];
+                            hw = i & 1 ? hw | h << 16 : h;
+                            lw = i & 1 ? lw | d << 16 : d;
+                        }
+                    }
+                    *reinterpret_cast<uint4 *>(pbuf + c * 8) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(pbuf + (HQP + c) * 8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                fence_async_smem();
+                tc_fence_before();
+                if (__syncthreads_or(!ok)) {   // a wait ran out
+                    ok = false;
+                    break;
+                }
+            }
+            if (ok) gwait(bar_pv, (uint32_t)(i1 - i0 - 1) & 1u, abort_flag);
+            tc_fence_after();
+
+            // the row's sums
+#pragma unroll
+            for (int i = 0; i < HG / 2; ++i) {
+                float2 v = up(l[i]);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+                    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+                }
+                if (lane == 0) *reinterpret_cast<float2 *>(gmax + quad * HG + 2 * i) = v;
+            }
+            bar_sync_n(2 + hg, 128);
+            if (quad == 0 && lane < HG) {
+                epi_l[h0 + lane] = (gmax[lane] + gmax[HG + lane]) + (gmax[2 * HG + lane] + gmax[3 * HG + lane]);
+                epi_m[h0 + lane] = m;
+            }
+            bar_sync_n(2 + hg, 128);
+            // O = O_hi + O_lo / 16; a part of a row stays unnormalised, for the merge (the
+            // K and V tiles are idle by now)
+            float *part = reinterpret_cast<float *>(sm + C::kOffK);
+            uint16_t *orow = A.out + (int64_t)r * A.Hq * D;
 #pragma unroll
             for (int c = 0; c < HG; c += 8) {
                 uint32_t u[8], v[8];
-                tmem_ld_x8(lane_t + (uint32_t)c, u);
-                tmem_ld_x8(lane_t + (uint32_t)(HQP + c), v);
+                tmem_ld_x8(lane_t + (uint32_t)(N2 + c), u);
+                tmem_ld_x8(lane_t + (uint32_t)(N2 + HQP + c), v);
                 tmem_ld_wait();
+                if (D == 128 || key < D) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const ulonglong2 n2 = nm[c / 4 + i / 2];
-                    const f2 x = add2(pku(u[2 * i], u[2 * i + 1]), pku(v[2 * i], v[2 * i + 1]));
-                    e[c / 2 + i] = fma2(x, c2, add2(lv2, i & 1 ? n2.y : n2.x));
-                    const float2 f = up(e[c / 2 + i]);
-                    emax = fmaxf(emax, fmaxf(f.x, f.y));
-                }
-            }
-            // One vote of the group a tile: does any head need a new maximum?
-            if (bar_or(1 + 2 * hg, 128, fresh || emax > kRaise)) {
-                float *gmax = reinterpret_cast<float *>(sm + C::kOffMax) + h0 * 4;   // [quad][16]
-#pragma unroll
-                for (int i = 0; i < HG / 2; ++i) {
-                    const float2 f = up(e[i]);
-                    const float x = redux_max(f.x), y = redux_max(f.y);
-                    if (lane == 0) *reinterpret_cast<float2 *>(gmax + quad * HG + 2 * i) = make_float2(x, y);
-                }
-                bar_sync_n(2 + 2 * hg, 128);
-                // a head a lane: how far its maximum goes up, and what that makes of the sums
-                float up_by = 0.f;
-                if (lane < HG) {
-                    const float tm = fmaxf(fmaxf(gmax[lane], gmax[HG + lane]), fmaxf(gmax[2 * HG + lane], gmax[3 * HG + lane]));
-                    if (tm > (fresh ? kLowest : kRaise)) up_by = tm - kTop;
-                }
-                const float f = ex2f(-up_by);
-                const bool resc = !fresh && __any_sync(0xffffffffu, up_by != 0.f);
-                if (lane < HG) negm[lane] -= up_by;
-#pragma unroll
-                for (int c = 0; c < HG; c += 8) {
-                    float fc[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) fc[k] = __shfl_sync(0xffffffffu, f, c + k);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float d0 = __shfl_sync(0xffffffffu, up_by, c + 2 * i), d1 = __shfl_sync(0xffffffffu, up_by, c + 2 * i + 1);
-                        e[c / 2 + i] = add2(e[c / 2 + i], pk(-d0, -d1));
-                        if (resc) l[c / 2 + i] = fma2(l[c / 2 + i], pk(fc[2 * i], fc[2 * i + 1]), 0);
-                    }
-                    if (resc) {   // P V(t - 1) is done: O holds the row's earlier tiles
-#pragma unroll
-                        for (int part = 0; part < 2; ++part) {
-                            uint32_t o[8];
-                            tmem_ld_x8(lane_t + (uint32_t)(N2 + part * HQP + c), o);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fc[k]);
-                            tmem_st8(lane_t + (uint32_t)(N2 + part * HQP + c), o);
+                    for (int k = 0; k < 8; ++k) {
+                        const int h = h0 + c + k;
+                        const float o = fmaf(__uint_as_float(v[k]), 0.0625f, __uint_as_float(u[k]));
+                        if (P.G > 1) {
+                            part[h * D + key] = o;
+                        } else if (h < A.Hq) {
+                            const float L = epi_l[h];
+                            const __nv_bfloat16 ob = __float2bfloat16_rn(o * (L == 0.f ? 0.f : 1.f / L));
+                            orow[(int64_t)h * D + key] = *reinterpret_cast<const uint16_t *>(&ob);
                         }
                     }
                 }
-                if (resc) tmem_st_wait_all();
-                if (fresh) fresh = !bar_or(1 + 2 * hg, 128, lv > -CUDART_INF_F);   // (only bad pages so far)
-                __syncwarp();
             }
-            // P^T as an MN-major operand without swizzle: 16-byte rows of 16 heads, the
-            // rows of 8 keys 16 bytes apart, the head chunks of a key group 128 bytes
-            // apart (first all high parts, then the low ones), key groups N2 * 8 bytes apart
-            uint8_t *pbuf = sm + C::kOffP + (key >> 3) * (N2 * 8) + (key & 7) * 16 + (h0 / 16) * 128;
-#pragma unroll
-            for (int c = 0; c < HG / 16; ++c) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 f = up(e[8 * c + i]);
-                    const float p0 = ex2f(f.x), p1 = ex2f(f.y);
-                    l[8 * c + i] = fma2(pk(p0, p1), iv2, l[8 * c + i]);
-                    const uint32_t p16 = f16x2(p0, p1), h = e4m3x2_of_f16(p16);
-                    const uint32_t d = e4m3x2_of_f16(hmul2(hsub2(p16, f16x2_of_e4m3(h)), 0x4C004C00u));   // the rest times 16
-                    hi[i / 2] = i & 1 ? hi[i / 2] | h << 16 : h;
-                    lo[i / 2] = i & 1 ? lo[i / 2] | d << 16 : d;
-                }
-                *reinterpret_cast<uint4 *>(pbuf + c * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(pbuf + (HQP / 16 + c) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (P.G == 1 && A.lse && quad == 0 && lane < HG && h0 + lane < A.Hq) {
+                const float L = epi_l[h0 + lane];
+                A.lse[(int64_t)r * A.Hq + h0 + lane] =
+                    L == 0.f ? -CUDART_INF_F : (epi_m[h0 + lane] + log2f(L)) * 0.69314718055994531f;
             }
-            if (tid < kTile && t + 1 < i1) {
-                put_scale(t + 1, row1, ks1, vs1);
-                row1 = put_row(t + 2, pos2, pg2);
-                pos2 = position(t + 3);
-            }
-            cp_async_wait_all();
-            fence_async_smem();
-            tc_fence_before();
-            if (__syncthreads_or(!ok)) {   // a wait ran out
-                ok = false;
-                break;
-            }
-            if (tid == 0) {
-                tc_fence_after();
-                issue_pv(t == i0);
-                if (t + 1 < i1) issue_s();
-                tc_commit(bar);
-            }
-            __syncwarp();
-        }
-        if (ok) ok = gwait(bar, (uint32_t)(i1 - i0) & 1u, abort_flag);
-        if (!ok && tid == 0) report(A.dev_status, SA_DEV_TIMEOUT);
-        tc_fence_after();
-
-        // ------------------------------------------------------------ the row's sums
-        float *gsum = reinterpret_cast<float *>(sm + C::kOffMax) + h0 * 4;
-#pragma unroll
-        for (int i = 0; i < HG / 2; ++i) {
-            float2 v = up(l[i]);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-                v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-            }
-            if (lane == 0) *reinterpret_cast<float2 *>(gsum + quad * HG + 2 * i) = v;
-        }
-        bar_sync_n(2 + 2 * hg, 128);
-        if (quad == 0 && lane < HG) {
-            epi_l[h0 + lane] = (gsum[lane] + gsum[HG + lane]) + (gsum[2 * HG + lane] + gsum[3 * HG + lane]);
-            epi_m[h0 + lane] = -negm[lane];
-        }
-        bar_sync_n(2 + 2 * hg, 128);
-        // O = O_hi + O_lo / 16; a part of a row stays unnormalised, for the merge (the
-        // K and V tiles are idle by now)
-        float *part = reinterpret_cast<float *>(sm + C::kOffK);
-        uint16_t *orow = A.out + (int64_t)r * A.Hq * D;
-#pragma unroll
-        for (int c = 0; c < HG; c += 8) {
-            uint32_t u[8], v[8];
-            tmem_ld_x8(lane_t + (uint32_t)(N2 + c), u);
-            tmem_ld_x8(lane_t + (uint32_t)(N2 + HQP + c), v);
-            tmem_ld_wait();
-            if (D == 128 || key < D) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int h = h0 + c + k;
-                    const float o = fmaf(__uint_as_float(v[k]), 0.0625f, __uint_as_float(u[k]));
-                    if (P.G > 1) {
-                        part[h * D + key] = o;
-                    } else if (h < A.Hq) {
-                        const float L = epi_l[h];
-                        const __nv_bfloat16 ob = __float2bfloat16_rn(o * (L == 0.f ? 0.f : 1.f / L));
-                        orow[(int64_t)h * D + key] = *reinterpret_cast<const uint16_t *>(&ob);
-                    }
-                }
-            }
-        }
-        if (P.G == 1 && A.lse && quad == 0 && lane < HG && h0 + lane < A.Hq) {
-            const float L = epi_l[h0 + lane];
-            A.lse[(int64_t)r * A.Hq + h0 + lane] =
-                L == 0.f ? -CUDART_INF_F : (epi_m[h0 + lane] + log2f(L)) * 0.69314718055994531f;
         }
     } else if (tid < HQP) {   // no share of the row
         epi_m[tid] = kLowest;
