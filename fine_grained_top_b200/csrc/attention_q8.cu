@@ -70,21 +70,26 @@ struct Cfg {
     static constexpr int kOffV = kOffK + kKV;
     static constexpr int kOffQ = kOffV + kKV;
     static constexpr int kOffP = kOffQ + kQ;
-    static constexpr int kOffRows = kOffP + kP;                       // [2][128] cache rows of a tile's keys
-    static constexpr int kOffSc = kOffRows + 2 * kTile * 4;           // [2][3][128] score factor, log2 vs, 1 / vs
+    static constexpr int kOffRows = kOffP + 2 * kP;                   // [4][128] cache rows of a tile's keys
+    static constexpr int kOffSc = kOffRows + 4 * kTile * 4;           // [2][3][128] score factor, log2 vs, 1 / vs
     static constexpr int kOffMax = kOffSc + 2 * 3 * kTile * 4;           // [4][HQP] maxima or sums of the quads
     static constexpr int kOffNegM = kOffMax + 4 * HQP * 4;            // [softmax warp][HG] minus the running maxima
     static constexpr int kOffEpi = kOffNegM + 4 * HQP * 4;            // m, l [2][HQP]
     static constexpr int kOffMerge = kOffEpi + 2 * HQP * 4;           // [2][HQP + 16] m, l of every CTA (clusters)
-    static constexpr int kOffMisc = kOffMerge + 2 * (HQP + 16) * 4;
+    static constexpr int kOffFlags = kOffMerge + 2 * (HQP + 16) * 4;  // [group][4] heads to raise, by eights
+    static constexpr int kOffMisc = kOffFlags + NG * 16;
     static constexpr int kUsed = 1024 + kOffMisc + 64;
-    static constexpr uint32_t kTmemCols = 2 * N2;                     // S, O
+    static constexpr uint32_t kTmemCols = 2 * HQP + N2;               // two S buffers, O
     // CTAs wait for TMEM columns while others of their cluster wait for them, so
     // whatever shares an SM must fit its 512 columns: shared memory in proportion.
     static constexpr int kLeast = (int)(kTmemCols * (kSmemSm / 512)) - 1024;
     static constexpr int kSmem = kUsed > kLeast ? kUsed : kLeast;
-    // CTAs an SM: two to four by their registers (80 a thread, 64 with 16 heads)
+    // CTAs an SM: two to four by their registers.  The loader warps hand most of
+    // theirs to the softmax warps.
     static constexpr int kByRegs = HQP == 16 ? 4 : (HQP == 32 ? 3 : 2);
+    static constexpr int kRegs = HQP == 16 ? 64 : 80, kRegsLoad = 40, kRegsSoft = HQP == 16 ? 88 : (HQP == 32 ? 120 : 96);
+    static_assert(kRegsLoad * 128 + kRegsSoft * 128 * NG <= kRegs * kThreads, "registers of the launch");
+    static_assert(kRegs * kThreads * kByRegs <= 65536, "registers of an SM");
     static constexpr int kPerSm = kSmemSm / (kSmem + 1024) < kByRegs ? kSmemSm / (kSmem + 1024) : kByRegs;
     static_assert(2 * kKV >= HQP * D * 4, "the partial O of a cluster's CTA lies in the K and V tiles");
 };
@@ -116,6 +121,22 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_x16(taddr, r); }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_x32(taddr, r); }
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
     asm volatile("{ .reg .pred p; .reg .b32 d; elect.sync d|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
@@ -148,15 +169,19 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint32_t e4m3x2_of_f16(uint32_t h) {
-    unsigned short r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+__device__ __forceinline__ uint32_t e4m3x4_of_f16(uint32_t a, uint32_t b) {   // a's pair in the low half
+    uint32_t r;
+    asm("{ .reg .b16 x, y; cvt.rn.satfinite.e4m3x2.f16x2 x, %1; cvt.rn.satfinite.e4m3x2.f16x2 y, %2; mov.b32 %0, {x, y}; }"
+        : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t c) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)c));
-    return h;
+__device__ __forceinline__ void f16_of_e4m3x4(uint32_t c, uint32_t &a, uint32_t &b) {
+    asm("{ .reg .b16 x, y; mov.b32 {x, y}, %2; cvt.rn.f16x2.e4m3x2 %0, x; cvt.rn.f16x2.e4m3x2 %1, y; }" : "=r"(a), "=r"(b) : "r"(c));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {   // NaN counts as absent
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -213,8 +238,8 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     float *sc = reinterpret_cast<float *>(sm + C::kOffSc);
     float *epi_m = reinterpret_cast<float *>(sm + C::kOffEpi), *epi_l = epi_m + HQP;
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + C::kOffMisc);
-    uint64_t *bar_s = bar, *bar_pv = bar + 1;   // S(t), P V(t) done
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 2);
+    uint64_t *bar_s = bar, *bar_pv = bar + 2;   // S(t) done, one for each S buffer; P V(t) done
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 3);
     int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
     unsigned *s_first = reinterpret_cast<unsigned *>(tmem_slot + 2), *s_qmax = s_first + 1;
 
@@ -242,6 +267,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     }
     if (tid == 0) {
         mbar_init(bar_s, 1);
+        mbar_init(bar_s + 1, 1);
         mbar_init(bar_pv, 1);
         *abort_flag = 0;
         *s_first = (unsigned)A.K;
@@ -255,7 +281,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);   // S (N2 columns), O (N2 columns)
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);   // S buffers (HQP columns each), O (N2 columns)
 
     int p = nv - 1;
     if (nv < 0 || nv > A.S_max) {
@@ -348,10 +374,10 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 else if (page >= 0 && page < A.pool_pages) row = page * 64 + (pos & 63);
                 else report(A.dev_status, SA_DEV_INDEX);
             }
-            // in the order the copies take them: key 16 i + c is number i of the c-th row of threads
-            rows[(t & 1) * kTile + (tid % RPT) * NIT + tid / RPT] = row;
-            return row;
+            // in the order the copies take them: key RPT i + c is number i of the c-th row of threads
+            rows[(t & 3) * kTile + (tid % RPT) * NIT + tid / RPT] = row;
         };
+        auto row_of = [&](int t) { return rows[(t & 3) * kTile + (tid % RPT) * NIT + tid / RPT]; };
         auto put_scale = [&](int t, int row, float ks, float vs) {
             vs = clamp_scale(vs);
             float *o = sc + (t & 1) * 3 * kTile + tid;
@@ -359,33 +385,36 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             o[kTile] = row >= 0 ? __log2f(vs) : -CUDART_INF_F;
             o[2 * kTile] = row >= 0 ? __frcp_rn(vs) : 0.f;
         };
-        int pos2 = -1, row1 = -1;   // the key of tile t + 2, the cache row of tile t + 1's
-        int ids[NIT];               // the rows that this thread copies of tile t
+        int pos3 = -1;   // the position of tile t + 3's key
         if (loader) {
-            const int pos0 = position(i0), pos1 = position(i0 + 1);
-            const int pg0 = page_of(pos0), pg1 = page_of(pos1);
-            pos2 = position(i0 + 2);
-            const int row0 = put_row(i0, pos0, pg0);
+            const int pos0 = position(i0), pos1 = position(i0 + 1), pos2 = position(i0 + 2);
+            const int pg0 = page_of(pos0), pg1 = page_of(pos1), pg2 = page_of(pos2);
+            pos3 = position(i0 + 3);
+            put_row(i0, pos0, pg0);
+            const int row0 = row_of(i0);
             float ks = 0.f, vs = 0.f;
             if (row0 >= 0) {
                 ks = __ldg(A.k_scale + (row0 >> P.sb_shift));
                 vs = __ldg(A.v_scale + (row0 >> P.sb_shift));
             }
-            row1 = put_row(i0 + 1, pos1, pg1);
+            put_row(i0 + 1, pos1, pg1);
+            put_row(i0 + 2, pos2, pg2);
             put_scale(i0, row0, ks, vs);
         }
         __syncthreads();
 
         // copies of a tile's rows, D / 16 threads a row
-        auto load_ids = [&](int t, int (&ids)[NIT]) {
+        auto gather = [&](int t, const uint8_t *src, int off) {
+            int ids[NIT];
 #pragma unroll
             for (int q = 0; q < NIT / 4; ++q)
-                reinterpret_cast<int4 *>(ids)[q] = reinterpret_cast<const int4 *>(rows + (t & 1) * kTile + (tid / CPH) * NIT)[q];
-        };
-        auto gather = [&](const uint8_t *src, int off, const int (&ids)[NIT], bool full) {
+                reinterpret_cast<int4 *>(ids)[q] = reinterpret_cast<const int4 *>(rows + (t & 3) * kTile + (tid / CPH) * NIT)[q];
+            int a = ids[0];
+#pragma unroll
+            for (int i = 1; i < NIT; ++i) a = min(a, ids[i]);
             const uint8_t *from = src + (tid % CPH) * 16;
             uint8_t *to = sm + off + sw<D>(tid / CPH, tid % CPH);   // RPT is a multiple of 8: one swizzle for all rows
-            if (full) {
+            if (__all_sync(0xffffffffu, a >= 0)) {
 #pragma unroll
                 for (int i = 0; i < NIT; ++i) cp_async16(to + i * RPT * D, from + (int64_t)ids[i] * D);
             } else {
@@ -394,18 +423,9 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     cp_async16_or_zero(to + i * RPT * D, from + (int64_t)max(ids[i], 0) * D, ids[i] >= 0);
             }
         };
-        bool full0 = false;   // tile t has no slot without a key
-        auto all_keys = [&](const int (&ids)[NIT]) {
-            int a = ids[0];
-#pragma unroll
-            for (int i = 1; i < NIT; ++i) a = min(a, ids[i]);
-            return __all_sync(0xffffffffu, a >= 0) != 0;
-        };
         if (loader) {
-            load_ids(i0, ids);
-            full0 = all_keys(ids);
-            gather(A.k, C::kOffK, ids, full0);
-            gather(A.v, C::kOffV, ids, full0);
+            gather(i0, A.k, C::kOffK);
+            gather(i0, A.v, C::kOffV);
         }
         // both parts of this thread's chunks of Q, while the copies fly (heads >= Hq are zeros)
 #pragma unroll
@@ -434,59 +454,80 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         fence_async_smem();
         __syncthreads();
 
-        auto issue_s = [&]() {
-            constexpr uint32_t idesc = idesc_e4m3_f32(128, N2);
+        auto issue_s = [&](int t) {   // both parts of Q into the same columns
+            constexpr uint32_t idesc = idesc_e4m3_f32(128, HQP);
             const uint64_t kd = smem_desc(smem_u32(sm + C::kOffK), 8 * D, D == 128 ? 2 : 4);
             const uint64_t qd = smem_desc(smem_u32(sm + C::kOffQ), 8 * D, D == 128 ? 2 : 4);
+            const uint32_t dt = tmem + (uint32_t)(((t - i0) & 1) * HQP);
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk)
-                tc_mma_f8(tmem, kd + (uint64_t)((kk * 32) >> 4), qd + (uint64_t)((kk * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int kk = 0; kk < D / 32; ++kk)
+                    tc_mma_f8(dt, kd + (uint64_t)((kk * 32) >> 4), qd + (uint64_t)((part * HQP * D + kk * 32) >> 4), idesc,
+                              part + kk > 0 ? 1u : 0u);
+            tc_commit(bar_s + ((t - i0) & 1));
         };
-        auto issue_pv = [&](bool first) {   // A (V^T) and B (P^T) both MN-major
+        auto issue_pv = [&](int t) {   // A (V^T) and B (P^T) both MN-major
             constexpr uint32_t idesc = idesc_e4m3_f32(128, N2) | (1u << 15) | (1u << 16);
             const uint64_t vd = desc_v<D>(smem_u32(sm + C::kOffV));
-            const uint64_t pd = desc_mn_plain(smem_u32(sm + C::kOffP), N2 * 8, 128);
+            const uint64_t pd = desc_mn_plain(smem_u32(sm + C::kOffP + ((t - i0) & 1) * C::kP), N2 * 8, 128);
 #pragma unroll
             for (int kk = 0; kk < kTile / 32; ++kk)   // 32 keys: four 8-key groups
-                tc_mma_f8(tmem + N2, vd + (uint64_t)((kk * 32 * D) >> 4), pd + (uint64_t)((kk * 4 * N2 * 8) >> 4), idesc,
-                          (first && kk == 0) ? 0u : 1u);
+                tc_mma_f8(tmem + 2 * HQP, vd + (uint64_t)((kk * 32 * D) >> 4), pd + (uint64_t)((kk * 4 * N2 * 8) >> 4), idesc,
+                          (t == i0 && kk == 0) ? 0u : 1u);
+            tc_commit(bar_pv);
         };
-        if (warp == 0 && elect_one()) {
-            issue_s();
-            tc_commit(bar_s);
-        }
+        if (warp == 0 && elect_one()) issue_s(i0);
         __syncwarp();
         bool ok = true;
+        // P V(t) is phase t - i0 of its barrier; S(t) may end while some warp still looks for
+        // the end of S(t - 1), so each S buffer has a barrier of its own
+        auto wait_s = [&](int t) { return mbar_wait(bar_s + ((t - i0) & 1), (uint32_t)((t - i0) >> 1) & 1u, abort_flag); };
+        auto wait_pv = [&](int t) { return mbar_wait(bar_pv, (uint32_t)(t - i0) & 1u, abort_flag); };
+        // Only loader warp 0 polls: warps that poll take issue slots from those that
+        // compute, and warps that wait at a barrier do not.
+        constexpr int kBarLoad = 1, kBarFirst = 6;
         if (loader) {
             // ------------------------------------------------------------ loader warps
+            regs_dec<C::kRegsLoad>();
+            if (i0 + 1 < i1) {
+                if (warp == 0) {
+                    ok = wait_s(i0);   // the K tile is free
+                    bar_arrive_n(kBarFirst, C::kThreads - 96);
+                }
+                bar_sync_n(kBarLoad, 128);
+                gather(i0 + 1, A.k, C::kOffK);
+                cp_async_wait_all();
+                fence_async_smem();
+                bar_sync_n(kBarLoad, 128);
+                if (warp == 0 && elect_one()) issue_s(i0 + 1);
+                __syncwarp();
+            } else if (warp == 0) {
+                ok = wait_s(i0);
+                bar_arrive_n(kBarFirst, C::kThreads - 96);
+            }
             for (int t = i0; t < i1; ++t) {
-                // lookups ahead: the page of tile t + 2's key, the scales of tile t + 1's
-                const int pg2 = page_of(pos2);
+                // lookups ahead: the page of tile t + 3's key, the scales of tile t + 1's
+                // (first: the products that the copies wait for run meanwhile)
+                const int pg3 = page_of(pos3), row1 = row_of(t + 1);
                 float ks1 = 0.f, vs1 = 0.f;
-                if (row1 >= 0) {
+                if (t + 1 < i1 && row1 >= 0) {
                     ks1 = __ldg(A.k_scale + (row1 >> P.sb_shift));
                     vs1 = __ldg(A.v_scale + (row1 >> P.sb_shift));
                 }
-                const int pos3 = position(t + 3);
-                ok = gwait(bar_s, (uint32_t)(t - i0) & 1u, abort_flag);   // the K tile is free
-                int ids1[NIT];
-                bool full1 = false;
-                if (t + 1 < i1) {
-                    load_ids(t + 1, ids1);
-                    full1 = all_keys(ids1);
-                    gather(A.k, C::kOffK, ids1, full1);
-                }
-                if (t > i0) {
-                    ok = ok && gwait(bar_pv, (uint32_t)(t - i0 - 1) & 1u, abort_flag);   // the V tile is free
-                    gather(A.v, C::kOffV, ids, full0);
-                }
+                const int pos4 = position(t + 4);
+                put_row(t + 3, pos3, pg3);
+                pos3 = pos4;
                 if (t + 1 < i1) {
                     put_scale(t + 1, row1, ks1, vs1);
-                    row1 = put_row(t + 2, pos2, pg2);
-                    pos2 = pos3;
-                    full0 = full1;
-#pragma unroll
-                    for (int i = 0; i < NIT; ++i) ids[i] = ids1[i];
+                    if (warp == 0) ok = ok && wait_s(t + 1);   // the K tile is free (and the softmax of t + 1 has its scores)
+                    bar_sync_n(kBarLoad, 128);
+                    if (t + 2 < i1) gather(t + 2, A.k, C::kOffK);
+                }
+                if (t > i0) {
+                    if (warp == 0) ok = ok && wait_pv(t - 1);   // the V tile is free (and the P tile of t + 1)
+                    bar_sync_n(kBarLoad, 128);
+                    gather(t, A.v, C::kOffV);
                 }
                 cp_async_wait_all();
                 fence_async_smem();
@@ -496,120 +537,154 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 }
                 if (warp == 0 && elect_one()) {
                     tc_fence_after();
-                    if (t + 1 < i1) {   // first: the softmax of t + 1 starts while P V(t) runs
-                        issue_s();
-                        tc_commit(bar_s);
-                    }
-                    issue_pv(t == i0);
-                    tc_commit(bar_pv);
+                    issue_pv(t);
+                    if (t + 2 < i1) issue_s(t + 2);
                 }
                 __syncwarp();
             }
-            if (ok) ok = gwait(bar_pv, (uint32_t)(i1 - i0 - 1) & 1u, abort_flag);
-            if (!ok && tid == 0) report(A.dev_status, SA_DEV_TIMEOUT);
+            if (warp == 0) {
+                if (ok) ok = wait_pv(i1 - 1);
+                if (!ok && lane == 0) report(A.dev_status, SA_DEV_TIMEOUT);
+                bar_arrive_n(kBarFirst, C::kThreads - 96);
+            }
+            regs_inc<C::kRegs>();
         } else {
             // ------------------------------------------------------------ softmax warps
+            regs_inc<C::kRegsSoft>();
             f2 l[HG / 2];
 #pragma unroll
             for (int i = 0; i < HG / 2; ++i) l[i] = 0;
             float *gmax = reinterpret_cast<float *>(sm + C::kOffMax) + h0 * 4;   // [quad][HG]
-            uint8_t *pbuf = sm + C::kOffP + (key >> 3) * (N2 * 8) + (key & 7) * 16 + (h0 / 16) * 128;
+            uint32_t *flags = reinterpret_cast<uint32_t *>(sm + C::kOffFlags) + 4 * hg;   // [quad]
+            uint8_t *pbuf0 = sm + C::kOffP + (key >> 3) * (N2 * 8) + (key & 7) * 16 + (h0 / 16) * 128;
             float m = kLowest;   // a head a lane: its running maximum
             if (lane < HG) negm[lane] = -m;
+            __syncwarp();
+            bar_sync_n(kBarFirst, C::kThreads - 96);   // S(i0) is done
             for (int t = i0; t < i1; ++t) {
-                ok = gwait(bar_s, (uint32_t)(t - i0) & 1u, abort_flag);
+                // S(t) is done, and P V(t - 2): the loader warps have waited for both
                 tc_fence_after();
+                const uint32_t s_t = lane_t + (uint32_t)(((t - i0) & 1) * HQP);
                 const float *kf = sc + (t & 1) * 3 * kTile + key;
                 const f2 c2 = pk(kf[0], kf[0]), lv2 = pk(kf[kTile], kf[kTile]), iv2 = pk(kf[2 * kTile], kf[2 * kTile]);
-                // Scores (with the value's scale, in log2) of 8 heads.  They are read from TMEM
-                // for the maxima and again for P: 32 registers less than keeping them.
-                auto scores = [&](int c, f2 (&x)[4]) {
-                    uint32_t u[8], v[8];
-                    tmem_ld_x8(lane_t + (uint32_t)c, u);
-                    tmem_ld_x8(lane_t + (uint32_t)(HQP + c), v);
+                // e: log2 of P
+                f2 e[HG / 2];
+                float top[HG / 8];   // the largest of each 8 heads
+                {
+                    uint32_t u[HG];
+                    tmem_ld_cols(s_t, u);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[i] = add2(pku(u[2 * i], u[2 * i + 1]), pku(v[2 * i], v[2 * i + 1]));
-                };
-                // the tile's maximum of every head, over this warp's keys and then the group's
-                float tm = -CUDART_INF_F;
+                    for (int c = 0; c < HG / 8; ++c) {
+                        const ulonglong2 n0 = reinterpret_cast<const ulonglong2 *>(negm + 8 * c)[0];
+                        const ulonglong2 n1 = reinterpret_cast<const ulonglong2 *>(negm + 8 * c)[1];
+                        const f2 nm[4] = {n0.x, n0.y, n1.x, n1.y};
+                        top[c] = -CUDART_INF_F;
 #pragma unroll
-                for (int c = 0; c < HG; c += 8) {
-                    f2 x[4];
-                    scores(c, x);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 f = up(fma2(x[i], c2, lv2));
-                        const float a = redux_max(f.x), b = redux_max(f.y);
-                        if (lane == c + 2 * i) tm = a;
-                        if (lane == c + 2 * i + 1) tm = b;
+                        for (int i = 0; i < 4; ++i) {
+                            e[4 * c + i] = fma2(pku(u[8 * c + 2 * i], u[8 * c + 2 * i + 1]), c2, add2(lv2, nm[i]));
+                            const float2 f = up(e[4 * c + i]);
+                            top[c] = max3(top[c], f.x, f.y);
+                        }
                     }
                 }
-                if (lane < HG) gmax[quad * HG + lane] = tm;
-                bar_sync_n(2 + hg, 128);
-                if (lane < HG) tm = fmaxf(fmaxf(gmax[lane], gmax[HG + lane]), fmaxf(gmax[2 * HG + lane], gmax[3 * HG + lane]));
-                if (t > i0) ok = ok && gwait(bar_pv, (uint32_t)(t - i0 - 1) & 1u, abort_flag);   // O and the P tile are free
-                tc_fence_after();
-                const bool raise = tm > m + kRaise;
-                const uint32_t raised = __ballot_sync(0xffffffffu, raise);
-                if (raised) {
-                    float f = 1.f;
-                    if (raise) {
-                        f = ex2f(m - (tm - kTop));
-                        m = tm - kTop;
-                        negm[lane] = -m;
-                    }
-                    if (t > i0) {   // what the row's earlier tiles made of these heads shrinks
+                float all = top[0];
 #pragma unroll
-                        for (int c = 0; c < HG; c += 8) {
-                            if (!((raised >> c) & 0xFFu)) continue;
+                for (int c = 1; c < HG / 8; ++c) all = fmaxf(all, top[c]);
+                // One vote of the group a tile: does any head need a new maximum?
+                if (bar_or(2 + 2 * hg, 128, all > kRaise)) {
+                    if (t > i0) ok = ok && wait_pv(t - 1);   // O is whole
+                    // which heads, by eights; their exact maxima over the tile's keys
+                    uint32_t eights = 0;
+#pragma unroll
+                    for (int c = 0; c < HG / 8; ++c) eights |= top[c] > kRaise ? 1u << c : 0u;
+                    eights = __reduce_or_sync(0xffffffffu, eights);
+                    if (lane == 0) flags[quad] = eights;
+                    bar_sync_n(3 + 2 * hg, 128);
+                    const uint4 fl = *reinterpret_cast<const uint4 *>(flags);
+                    eights = fl.x | fl.y | fl.z | fl.w;
+#pragma unroll
+                    for (int c = 0; c < HG / 8; ++c) {
+                        if (!((eights >> c) & 1u)) continue;
+                        uint32_t u[8];
+                        tmem_ld_x8(s_t + 8 * c, u);
+                        tmem_ld_wait();
+                        float mine = -CUDART_INF_F;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 f = up(fma2(pku(u[2 * i], u[2 * i + 1]), c2, lv2));
+                            const float x = redux_max(f.x), y = redux_max(f.y);
+                            if ((lane & 7) == 2 * i) mine = x;
+                            if ((lane & 7) == 2 * i + 1) mine = y;
+                        }
+                        if (lane < 8) gmax[quad * HG + 8 * c + lane] = mine;
+                    }
+                    bar_sync_n(3 + 2 * hg, 128);
+                    float f = 1.f;
+                    if (lane < HG && ((eights >> (lane >> 3)) & 1u)) {
+                        const float tm = fmaxf(fmaxf(gmax[lane], gmax[HG + lane]), fmaxf(gmax[2 * HG + lane], gmax[3 * HG + lane]));
+                        if (tm > m + kRaise) {
+                            f = ex2f(m - (tm - kTop));
+                            m = tm - kTop;
+                            negm[lane] = -m;
+                        }
+                    }
+                    __syncwarp();
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < HG / 8; ++c) {
+                        if (!((eights >> c) & 1u)) continue;
+                        uint32_t u[8];
+                        tmem_ld_x8(s_t + 8 * c, u);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            e[4 * c + i] = fma2(pku(u[2 * i], u[2 * i + 1]), c2,
+                                                add2(lv2, *reinterpret_cast<const f2 *>(negm + 8 * c + 2 * i)));
+                        if (t > i0) {   // what the row's earlier tiles made of these heads shrinks
                             float fc[8];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) fc[k] = __shfl_sync(0xffffffffu, f, c + k);
+                            for (int k = 0; k < 8; ++k) fc[k] = __shfl_sync(0xffffffffu, f, 8 * c + k);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) l[c / 2 + i] = fma2(l[c / 2 + i], pk(fc[2 * i], fc[2 * i + 1]), 0);
+                            for (int i = 0; i < 4; ++i) l[4 * c + i] = fma2(l[4 * c + i], pk(fc[2 * i], fc[2 * i + 1]), 0);
 #pragma unroll
                             for (int part = 0; part < 2; ++part) {
                                 uint32_t o[8];
-                                tmem_ld_x8(lane_t + (uint32_t)(N2 + part * HQP + c), o);
+                                tmem_ld_x8(lane_t + (uint32_t)(2 * HQP + part * HQP + 8 * c), o);
                                 tmem_ld_wait();
 #pragma unroll
                                 for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fc[k]);
-                                tmem_st8(lane_t + (uint32_t)(N2 + part * HQP + c), o);
+                                tmem_st8(lane_t + (uint32_t)(2 * HQP + part * HQP + 8 * c), o);
                             }
                         }
-                        tmem_st_wait_all();
                     }
-                    __syncwarp();
+                    tmem_st_wait_all();
                 }
                 // P^T as an MN-major operand without swizzle: 16-byte rows of 16 heads, the
                 // rows of 8 keys 16 bytes apart, the head chunks of a key group 128 bytes
                 // apart (first all high parts, then the low ones), key groups N2 * 8 bytes apart
+                uint8_t *pbuf = pbuf0 + ((t - i0) & 1) * C::kP;
 #pragma unroll
-                for (int c = 0; c < HG; c += 16) {
+                for (int c = 0; c < HG / 16; ++c) {
                     uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        f2 x[4];
-                        scores(c + 8 * half, x);
-                        const ulonglong2 n0 = reinterpret_cast<const ulonglong2 *>(negm + c + 8 * half)[0];
-                        const ulonglong2 n1 = reinterpret_cast<const ulonglong2 *>(negm + c + 8 * half)[1];
-                        const f2 nm[4] = {n0.x, n0.y, n1.x, n1.y};
+                    for (int i = 0; i < 4; ++i) {   // four heads
+                        uint32_t p16[2], h16[2];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 f = up(fma2(x[i], c2, add2(lv2, nm[i])));   // log2 of P
+                        for (int k = 0; k < 2; ++k) {
+                            const float2 f = up(e[8 * c + 2 * i + k]);
                             const float p0 = ex2f(f.x), p1 = ex2f(f.y);
-                            f2 &sum = l[c / 2 + 4 * half + i];
+                            f2 &sum = l[8 * c + 2 * i + k];
                             sum = fma2(pk(p0, p1), iv2, sum);
-                            const uint32_t p16 = f16x2(p0, p1), h = e4m3x2_of_f16(p16);
-                            const uint32_t d = e4m3x2_of_f16(hmul2(hsub2(p16, f16x2_of_e4m3(h)), 0x4C004C00u));   // the rest times 16
-                            uint32_t &hw = hi[2 * half + i / 2], &lw = lo[2 * half + i / 2];
-                            hw = i & 1 ? hw | h << 16 : h;
-                            lw = i & 1 ? lw | d << 16 : d;
+                            p16[k] = f16x2(p0, p1);
                         }
+                        hi[i] = e4m3x4_of_f16(p16[0], p16[1]);
+                        f16_of_e4m3x4(hi[i], h16[0], h16[1]);
+                        // the rest (exact) times 16
+                        lo[i] = e4m3x4_of_f16(hmul2(hsub2(p16[0], h16[0]), 0x4C004C00u), hmul2(hsub2(p16[1], h16[1]), 0x4C004C00u));
                     }
-                    *reinterpret_cast<uint4 *>(pbuf + c * 8) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(pbuf + (HQP + c) * 8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    *reinterpret_cast<uint4 *>(pbuf + c * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(pbuf + (HQP / 16 + c) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 fence_async_smem();
                 tc_fence_before();
@@ -618,26 +693,39 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     break;
                 }
             }
-            if (ok) gwait(bar_pv, (uint32_t)(i1 - i0 - 1) & 1u, abort_flag);
+            bar_sync_n(kBarFirst, C::kThreads - 96);   // P V of the last tile is done
             tc_fence_after();
 
-            // the row's sums
+            // the row's sums over this warp's keys, each step on half as many heads as the
+            // last: a lane ends with the sum of one head (HG = 16: of one half of the lanes)
+            float v[HG];
 #pragma unroll
             for (int i = 0; i < HG / 2; ++i) {
-                float2 v = up(l[i]);
+                const float2 f = up(l[i]);
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-                    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+            for (int o = HG / 2; o > 0; o >>= 1) {
+                const bool high = lane & o;
+#pragma unroll
+                for (int i = 0; i < o; ++i) {
+                    const float give = high ? v[i] : v[i + o], keep = high ? v[i + o] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
                 }
-                if (lane == 0) *reinterpret_cast<float2 *>(gmax + quad * HG + 2 * i) = v;
             }
-            bar_sync_n(2 + hg, 128);
+            if (HG == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
+            if (lane < HG) gmax[quad * HG + lane] = v[0];
+            bar_sync_n(3 + 2 * hg, 128);
             if (quad == 0 && lane < HG) {
-                epi_l[h0 + lane] = (gmax[lane] + gmax[HG + lane]) + (gmax[2 * HG + lane] + gmax[3 * HG + lane]);
-                epi_m[h0 + lane] = m;
+                const float L = (gmax[lane] + gmax[HG + lane]) + (gmax[2 * HG + lane] + gmax[3 * HG + lane]);
+                const int h = h0 + lane;
+                epi_m[h] = P.G > 1 ? m : (L == 0.f ? 0.f : 1.f / L);   // (whole rows need no m any more)
+                epi_l[h] = L;
+                if (P.G == 1 && A.lse && h < A.Hq)
+                    A.lse[(int64_t)r * A.Hq + h] = L == 0.f ? -CUDART_INF_F : (m + log2f(L)) * 0.69314718055994531f;
             }
-            bar_sync_n(2 + hg, 128);
+            bar_sync_n(3 + 2 * hg, 128);
             // O = O_hi + O_lo / 16; a part of a row stays unnormalised, for the merge (the
             // K and V tiles are idle by now)
             float *part = reinterpret_cast<float *>(sm + C::kOffK);
@@ -645,8 +733,8 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
 #pragma unroll
             for (int c = 0; c < HG; c += 8) {
                 uint32_t u[8], v[8];
-                tmem_ld_x8(lane_t + (uint32_t)(N2 + c), u);
-                tmem_ld_x8(lane_t + (uint32_t)(N2 + HQP + c), v);
+                tmem_ld_x8(lane_t + (uint32_t)(2 * HQP + c), u);
+                tmem_ld_x8(lane_t + (uint32_t)(3 * HQP + c), v);
                 tmem_ld_wait();
                 if (D == 128 || key < D) {
 #pragma unroll
@@ -656,18 +744,13 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                         if (P.G > 1) {
                             part[h * D + key] = o;
                         } else if (h < A.Hq) {
-                            const float L = epi_l[h];
-                            const __nv_bfloat16 ob = __float2bfloat16_rn(o * (L == 0.f ? 0.f : 1.f / L));
+                            const __nv_bfloat16 ob = __float2bfloat16_rn(o * epi_m[h]);
                             orow[(int64_t)h * D + key] = *reinterpret_cast<const uint16_t *>(&ob);
                         }
                     }
                 }
             }
-            if (P.G == 1 && A.lse && quad == 0 && lane < HG && h0 + lane < A.Hq) {
-                const float L = epi_l[h0 + lane];
-                A.lse[(int64_t)r * A.Hq + h0 + lane] =
-                    L == 0.f ? -CUDART_INF_F : (epi_m[h0 + lane] + log2f(L)) * 0.69314718055994531f;
-            }
+            regs_dec<C::kRegs>();
         }
     } else if (tid < HQP) {   // no share of the row
         epi_m[tid] = kLowest;
@@ -733,6 +816,12 @@ sa_status launch_q8(const AttnQ8Args &a, cudaStream_t st) {
     while ((1 << p.sb_shift) < a.scale_block) ++p.sb_shift;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     if (prepare_kernel<attn_q8_kernel<D, HQP>>(C::kSmem, p.G > 8) != cudaSuccess) return SA_ERR_CUDA;
+    // the warps' register shares are taken from what the launch gives its threads
+    static const int regs = [] {
+        cudaFuncAttributes f;
+        return cudaFuncGetAttributes(&f, attn_q8_kernel<D, HQP>) == cudaSuccess ? f.numRegs : 0;
+    }();
+    if (regs < C::kRegs) return SA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)R * (unsigned)p.G);
     cfg.blockDim = dim3(C::kThreads);

@@ -57,6 +57,8 @@ __device__ __forceinline__ bool iwait(uint64_t *bar, uint32_t parity, volatile i
     }
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// Arrive at barrier `id` without waiting for it.
+__device__ __forceinline__ void bar_arrive_n(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 // Barrier `id` over `n` threads that also returns the OR / AND of a predicate.
 __device__ __forceinline__ bool bar_or(int id, int n, bool p) {
     uint32_t r;
