@@ -67,10 +67,10 @@ struct Cfg {
     static constexpr int kThreads = 128 + 128 * NG;       // loader warps, softmax warps
     static constexpr int kKV = kTile * D, kQ = N2 * D, kP = kTile * N2;
     static constexpr int kOffK = 0;
-    static constexpr int kOffV = kOffK + kKV;
-    static constexpr int kOffQ = kOffV + kKV;
+    static constexpr int kOffV = kOffK + 2 * kKV;                     // two K tiles, two V tiles
+    static constexpr int kOffQ = kOffV + 2 * kKV;
     static constexpr int kOffP = kOffQ + kQ;
-    static constexpr int kOffRows = kOffP + 2 * kP;                   // [4][128] cache rows of a tile's keys
+    static constexpr int kOffRows = kOffP + kP;                   // [4][128] cache rows of a tile's keys
     static constexpr int kOffSc = kOffRows + 4 * kTile * 4;           // [2][3][128] score factor, log2 vs, 1 / vs
     static constexpr int kOffMax = kOffSc + 2 * 3 * kTile * 4;           // [4][HQP] maxima or sums of the quads
     static constexpr int kOffNegM = kOffMax + 4 * HQP * 4;            // [softmax warp][HG] minus the running maxima
@@ -78,7 +78,7 @@ struct Cfg {
     static constexpr int kOffMerge = kOffEpi + 2 * HQP * 4;           // [2][HQP + 16] m, l of every CTA (clusters)
     static constexpr int kOffFlags = kOffMerge + 2 * (HQP + 16) * 4;  // [group][4] heads to raise, by eights
     static constexpr int kOffMisc = kOffFlags + NG * 16;
-    static constexpr int kUsed = 1024 + kOffMisc + 64;
+    static constexpr int kUsed = kOffMisc + 64;
     static constexpr uint32_t kTmemCols = 2 * HQP + N2;               // two S buffers, O
     // CTAs wait for TMEM columns while others of their cluster wait for them, so
     // whatever shares an SM must fit its 512 columns: shared memory in proportion.
@@ -91,7 +91,7 @@ struct Cfg {
     static_assert(kRegsLoad * 128 + kRegsSoft * 128 * NG <= kRegs * kThreads, "registers of the launch");
     static_assert(kRegs * kThreads * kByRegs <= 65536, "registers of an SM");
     static constexpr int kPerSm = kSmemSm / (kSmem + 1024) < kByRegs ? kSmemSm / (kSmem + 1024) : kByRegs;
-    static_assert(2 * kKV >= HQP * D * 4, "the partial O of a cluster's CTA lies in the K and V tiles");
+    static_assert(4 * kKV >= HQP * D * 4, "the partial O of a cluster's CTA lies in the K and V tiles");
 };
 
 // ------------------------------------------------------------------ helpers
@@ -232,8 +232,7 @@ template <int D, int HQP>
 __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) attn_q8_kernel(Params P) {
     using C = Cfg<D, HQP>;
     constexpr int N2 = C::N2, NT = C::kThreads, HG = C::HG;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t sm[];   // (no static shared memory: it begins 1024-byte aligned)
     int32_t *rows = reinterpret_cast<int32_t *>(sm + C::kOffRows);
     float *sc = reinterpret_cast<float *>(sm + C::kOffSc);
     float *epi_m = reinterpret_cast<float *>(sm + C::kOffEpi), *epi_l = epi_m + HQP;
@@ -241,7 +240,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     uint64_t *bar_s = bar, *bar_pv = bar + 2;   // S(t) done, one for each S buffer; P V(t) done
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 3);
     int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
-    unsigned *s_first = reinterpret_cast<unsigned *>(tmem_slot + 2), *s_qmax = s_first + 1;
+    unsigned *s_first = reinterpret_cast<unsigned *>(tmem_slot + 2), *s_qmax = s_first + 1, *s_qodd = s_first + 2;
 
     const AttnQ8Args &A = P.a;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -272,6 +271,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         *abort_flag = 0;
         *s_first = (unsigned)A.K;
         *s_qmax = 0;
+        *s_qodd = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -315,14 +315,16 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         if (rank == 0 && bad_idx) report(A.dev_status, SA_DEV_INDEX);
         if (rank == 0 && bad_ord) report(A.dev_status, SA_DEV_ORDER);
         first_out = (int)__reduce_min_sync(0xffffffffu, (unsigned)first_out);
-        uint32_t mx = 0;   // largest finite |q|
+        uint32_t mx = 0, odd = 0;   // largest finite |q|; any infinite or NaN
 #pragma unroll
         for (int i = 0; i < 2 * NQ; ++i) {
             const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint32_t t = w[k] & 0x7FFF7FFFu;
-                mx = __vmaxu2(mx, t & __vcmpltu2(t, 0x7F807F80u));
+                const uint32_t fin = __vcmpltu2(t, 0x7F807F80u);
+                mx = __vmaxu2(mx, t & fin);
+                odd |= ~fin;
             }
         }
         mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
@@ -330,6 +332,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             atomicMin(s_first, (unsigned)first_out);
             atomicMax(s_qmax, mx);
         }
+        if (odd) *s_qodd = 1;
     }
     __syncthreads();
     const int n_top = p >= 0 ? (int)*s_first : 0;
@@ -413,7 +416,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
 #pragma unroll
             for (int i = 1; i < NIT; ++i) a = min(a, ids[i]);
             const uint8_t *from = src + (tid % CPH) * 16;
-            uint8_t *to = sm + off + sw<D>(tid / CPH, tid % CPH);   // RPT is a multiple of 8: one swizzle for all rows
+            uint8_t *to = sm + off + ((t - i0) & 1) * C::kKV + sw<D>(tid / CPH, tid % CPH);   // RPT is a multiple of 8: one swizzle for all rows
             if (__all_sync(0xffffffffu, a >= 0)) {
 #pragma unroll
                 for (int i = 0; i < NIT; ++i) cp_async16(to + i * RPT * D, from + (int64_t)ids[i] * D);
@@ -426,6 +429,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         if (loader) {
             gather(i0, A.k, C::kOffK);
             gather(i0, A.v, C::kOffV);
+            if (i0 + 1 < i1) gather(i0 + 1, A.k, C::kOffK);
         }
         // both parts of this thread's chunks of Q, while the copies fly (heads >= Hq are zeros)
 #pragma unroll
@@ -436,16 +440,21 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
             uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                float x = __uint_as_float(w[k] << 16) * down, y = __uint_as_float(w[k] & 0xFFFF0000u) * down;
-                // an infinite q makes NaN scores, as the formula does
-                if (!(fabsf(x) <= 448.f)) x = CUDART_NAN_F;
-                if (!(fabsf(y) <= 448.f)) y = CUDART_NAN_F;
-                const uint32_t h = e4m3x2(x, y);
-                const float2 f = from_e4m3x2(h);
-                const uint32_t e = e4m3x2(x - f.x, y - f.y);
-                hi[k / 2] = k & 1 ? hi[k / 2] | h << 16 : h;
-                lo[k / 2] = k & 1 ? lo[k / 2] | e << 16 : e;
+            for (int k = 0; k < 4; ++k) {
+                uint32_t y[2], h[2];   // scaled q in fp16: exact but for what is 2^-23 of the largest
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t x = w[2 * k + j];
+                    y[j] = f16x2(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xFFFF0000u) * down);
+                }
+                hi[k] = e4m3x4_of_f16(y[0], y[1]);
+                f16_of_e4m3x4(hi[k], h[0], h[1]);
+                lo[k] = e4m3x4_of_f16(hsub2(y[0], h[0]), hsub2(y[1], h[1]));
+                if (*s_qodd) {   // an infinite q makes NaN scores, as the formula does
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (((w[2 * k + j / 2] >> (16 * (j & 1))) & 0x7F80u) == 0x7F80u) hi[k] |= 0x7Fu << (8 * j);
+                }
             }
             *reinterpret_cast<uint4 *>(sm + C::kOffQ + sw<D>(c / CPH, c % CPH)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4 *>(sm + C::kOffQ + sw<D>(HQP + c / CPH, c % CPH)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -456,7 +465,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
 
         auto issue_s = [&](int t) {   // both parts of Q into the same columns
             constexpr uint32_t idesc = idesc_e4m3_f32(128, HQP);
-            const uint64_t kd = smem_desc(smem_u32(sm + C::kOffK), 8 * D, D == 128 ? 2 : 4);
+            const uint64_t kd = smem_desc(smem_u32(sm + C::kOffK + ((t - i0) & 1) * C::kKV), 8 * D, D == 128 ? 2 : 4);
             const uint64_t qd = smem_desc(smem_u32(sm + C::kOffQ), 8 * D, D == 128 ? 2 : 4);
             const uint32_t dt = tmem + (uint32_t)(((t - i0) & 1) * HQP);
 #pragma unroll
@@ -469,15 +478,18 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         };
         auto issue_pv = [&](int t) {   // A (V^T) and B (P^T) both MN-major
             constexpr uint32_t idesc = idesc_e4m3_f32(128, N2) | (1u << 15) | (1u << 16);
-            const uint64_t vd = desc_v<D>(smem_u32(sm + C::kOffV));
-            const uint64_t pd = desc_mn_plain(smem_u32(sm + C::kOffP + ((t - i0) & 1) * C::kP), N2 * 8, 128);
+            const uint64_t vd = desc_v<D>(smem_u32(sm + C::kOffV + ((t - i0) & 1) * C::kKV));
+            const uint64_t pd = desc_mn_plain(smem_u32(sm + C::kOffP), N2 * 8, 128);
 #pragma unroll
             for (int kk = 0; kk < kTile / 32; ++kk)   // 32 keys: four 8-key groups
                 tc_mma_f8(tmem + 2 * HQP, vd + (uint64_t)((kk * 32 * D) >> 4), pd + (uint64_t)((kk * 4 * N2 * 8) >> 4), idesc,
                           (t == i0 && kk == 0) ? 0u : 1u);
             tc_commit(bar_pv);
         };
-        if (warp == 0 && elect_one()) issue_s(i0);
+        if (warp == 0 && elect_one()) {
+            issue_s(i0);
+            if (i0 + 1 < i1) issue_s(i0 + 1);
+        }
         __syncwarp();
         bool ok = true;
         // P V(t) is phase t - i0 of its barrier; S(t) may end while some warp still looks for
@@ -486,29 +498,17 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         auto wait_pv = [&](int t) { return mbar_wait(bar_pv, (uint32_t)(t - i0) & 1u, abort_flag); };
         // Only loader warp 0 polls: warps that poll take issue slots from those that
         // compute, and warps that wait at a barrier do not.
-        constexpr int kBarLoad = 1, kBarFirst = 6;
+        constexpr int kBarLoad = 1, kBarSoft = 6, kSoft = C::kThreads - 96;   // loader warp 0 and the softmax warps
         if (loader) {
             // ------------------------------------------------------------ loader warps
             regs_dec<C::kRegsLoad>();
-            if (i0 + 1 < i1) {
-                if (warp == 0) {
-                    ok = wait_s(i0);   // the K tile is free
-                    bar_arrive_n(kBarFirst, C::kThreads - 96);
-                }
-                bar_sync_n(kBarLoad, 128);
-                gather(i0 + 1, A.k, C::kOffK);
-                cp_async_wait_all();
-                fence_async_smem();
-                bar_sync_n(kBarLoad, 128);
-                if (warp == 0 && elect_one()) issue_s(i0 + 1);
-                __syncwarp();
-            } else if (warp == 0) {
-                ok = wait_s(i0);
-                bar_arrive_n(kBarFirst, C::kThreads - 96);
-            }
             for (int t = i0; t < i1; ++t) {
+                // the scores of the first tile, or P V(t - 1): O and the P tile are free for the softmax
+                if (warp == 0) {
+                    ok = ok && (t == i0 ? wait_s(t) : wait_pv(t - 1));
+                    bar_arrive_n(kBarSoft, kSoft);
+                }
                 // lookups ahead: the page of tile t + 3's key, the scales of tile t + 1's
-                // (first: the products that the copies wait for run meanwhile)
                 const int pg3 = page_of(pos3), row1 = row_of(t + 1);
                 float ks1 = 0.f, vs1 = 0.f;
                 if (t + 1 < i1 && row1 >= 0) {
@@ -516,21 +516,18 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     vs1 = __ldg(A.v_scale + (row1 >> P.sb_shift));
                 }
                 const int pos4 = position(t + 4);
+                // the K tile t + 2 replaces is done with (S(t)), and the V tile t + 1 replaces (P V(t - 1))
+                bar_sync_n(kBarLoad, 128);
+                if (t + 2 < i1) gather(t + 2, A.k, C::kOffK);
+                if (t + 1 < i1) {
+                    gather(t + 1, A.v, C::kOffV);
+                    put_scale(t + 1, row1, ks1, vs1);
+                }
                 put_row(t + 3, pos3, pg3);
                 pos3 = pos4;
-                if (t + 1 < i1) {
-                    put_scale(t + 1, row1, ks1, vs1);
-                    if (warp == 0) ok = ok && wait_s(t + 1);   // the K tile is free (and the softmax of t + 1 has its scores)
-                    bar_sync_n(kBarLoad, 128);
-                    if (t + 2 < i1) gather(t + 2, A.k, C::kOffK);
-                }
-                if (t > i0) {
-                    if (warp == 0) ok = ok && wait_pv(t - 1);   // the V tile is free (and the P tile of t + 1)
-                    bar_sync_n(kBarLoad, 128);
-                    gather(t, A.v, C::kOffV);
-                }
                 cp_async_wait_all();
                 fence_async_smem();
+                if (warp == 0 && t + 1 < i1) ok = ok && wait_s(t + 1);   // the softmax of t + 1 has its scores
                 if (__syncthreads_or(!ok)) {   // a wait ran out
                     ok = false;
                     break;
@@ -545,7 +542,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             if (warp == 0) {
                 if (ok) ok = wait_pv(i1 - 1);
                 if (!ok && lane == 0) report(A.dev_status, SA_DEV_TIMEOUT);
-                bar_arrive_n(kBarFirst, C::kThreads - 96);
+                bar_arrive_n(kBarSoft, kSoft);
             }
             regs_inc<C::kRegs>();
         } else {
@@ -556,45 +553,64 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             for (int i = 0; i < HG / 2; ++i) l[i] = 0;
             float *gmax = reinterpret_cast<float *>(sm + C::kOffMax) + h0 * 4;   // [quad][HG]
             uint32_t *flags = reinterpret_cast<uint32_t *>(sm + C::kOffFlags) + 4 * hg;   // [quad]
-            uint8_t *pbuf0 = sm + C::kOffP + (key >> 3) * (N2 * 8) + (key & 7) * 16 + (h0 / 16) * 128;
+            uint8_t *pbuf = sm + C::kOffP + (key >> 3) * (N2 * 8) + (key & 7) * 16 + (h0 / 16) * 128;
             float m = kLowest;   // a head a lane: its running maximum
             if (lane < HG) negm[lane] = -m;
-            __syncwarp();
-            bar_sync_n(kBarFirst, C::kThreads - 96);   // S(i0) is done
+            bool fresh = true;                         // no key yet
+            bar_sync_n(kBarSoft, kSoft);               // S(i0) is done
             for (int t = i0; t < i1; ++t) {
-                // S(t) is done, and P V(t - 2): the loader warps have waited for both
+                // S(t) is done: loader warp 0 has waited for it
                 tc_fence_after();
                 const uint32_t s_t = lane_t + (uint32_t)(((t - i0) & 1) * HQP);
                 const float *kf = sc + (t & 1) * 3 * kTile + key;
                 const f2 c2 = pk(kf[0], kf[0]), lv2 = pk(kf[kTile], kf[kTile]), iv2 = pk(kf[2 * kTile], kf[2 * kTile]);
+                uint32_t u[HG];
+                tmem_ld_cols(s_t, u);
+                tmem_ld_wait();
+                if (fresh) {
+                    // the row's first keys: their exact maxima, so that the largest P is 2
+                    float tm = -CUDART_INF_F;
+#pragma unroll
+                    for (int i = 0; i < HG / 2; ++i) {
+                        const float2 f = up(fma2(pku(u[2 * i], u[2 * i + 1]), c2, lv2));
+                        const float x = redux_max(f.x), y = redux_max(f.y);
+                        if (lane == 2 * i) tm = x;
+                        if (lane == 2 * i + 1) tm = y;
+                    }
+                    if (lane < HG) gmax[quad * HG + lane] = tm;
+                    fresh = !bar_or(3 + 2 * hg, 128, kf[kTile] > -CUDART_INF_F);   // (only bad pages so far)
+                    if (lane < HG) {
+                        tm = fmaxf(fmaxf(gmax[lane], gmax[HG + lane]), fmaxf(gmax[2 * HG + lane], gmax[3 * HG + lane]));
+                        if (tm > kLowest) m = tm - kTop;
+                        negm[lane] = -m;
+                    }
+                    __syncwarp();
+                }
                 // e: log2 of P
                 f2 e[HG / 2];
                 float top[HG / 8];   // the largest of each 8 heads
-                {
-                    uint32_t u[HG];
-                    tmem_ld_cols(s_t, u);
-                    tmem_ld_wait();
 #pragma unroll
-                    for (int c = 0; c < HG / 8; ++c) {
-                        const ulonglong2 n0 = reinterpret_cast<const ulonglong2 *>(negm + 8 * c)[0];
-                        const ulonglong2 n1 = reinterpret_cast<const ulonglong2 *>(negm + 8 * c)[1];
-                        const f2 nm[4] = {n0.x, n0.y, n1.x, n1.y};
-                        top[c] = -CUDART_INF_F;
+                for (int c = 0; c < HG / 8; ++c) {
+                    const ulonglong2 n0 = reinterpret_cast<const ulonglong2 *>(negm + 8 * c)[0];
+                    const ulonglong2 n1 = reinterpret_cast<const ulonglong2 *>(negm + 8 * c)[1];
+                    const f2 nm[4] = {n0.x, n0.y, n1.x, n1.y};
+                    top[c] = -CUDART_INF_F;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            e[4 * c + i] = fma2(pku(u[8 * c + 2 * i], u[8 * c + 2 * i + 1]), c2, add2(lv2, nm[i]));
-                            const float2 f = up(e[4 * c + i]);
-                            top[c] = max3(top[c], f.x, f.y);
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        e[4 * c + i] = fma2(pku(u[8 * c + 2 * i], u[8 * c + 2 * i + 1]), c2, add2(lv2, nm[i]));
+                        const float2 f = up(e[4 * c + i]);
+                        top[c] = max3(top[c], f.x, f.y);
                     }
                 }
                 float all = top[0];
 #pragma unroll
                 for (int c = 1; c < HG / 8; ++c) all = fmaxf(all, top[c]);
                 // One vote of the group a tile: does any head need a new maximum?
-                if (bar_or(2 + 2 * hg, 128, all > kRaise)) {
-                    if (t > i0) ok = ok && wait_pv(t - 1);   // O is whole
+                const bool raise = bar_or(2 + 2 * hg, 128, all > kRaise);
+                if (t > i0) bar_sync_n(kBarSoft, kSoft);   // P V(t - 1) is done: O is whole, the P tile is free
+                if (raise) {
                     // which heads, by eights; their exact maxima over the tile's keys
+                    tc_fence_after();
                     uint32_t eights = 0;
 #pragma unroll
                     for (int c = 0; c < HG / 8; ++c) eights |= top[c] > kRaise ? 1u << c : 0u;
@@ -603,50 +619,43 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     bar_sync_n(3 + 2 * hg, 128);
                     const uint4 fl = *reinterpret_cast<const uint4 *>(flags);
                     eights = fl.x | fl.y | fl.z | fl.w;
+                    float mine = -CUDART_INF_F;
 #pragma unroll
                     for (int c = 0; c < HG / 8; ++c) {
                         if (!((eights >> c) & 1u)) continue;
-                        uint32_t u[8];
-                        tmem_ld_x8(s_t + 8 * c, u);
-                        tmem_ld_wait();
-                        float mine = -CUDART_INF_F;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float2 f = up(fma2(pku(u[2 * i], u[2 * i + 1]), c2, lv2));
+                            const float2 f = up(e[4 * c + i]);
                             const float x = redux_max(f.x), y = redux_max(f.y);
-                            if ((lane & 7) == 2 * i) mine = x;
-                            if ((lane & 7) == 2 * i + 1) mine = y;
+                            if (lane == 8 * c + 2 * i) mine = x;
+                            if (lane == 8 * c + 2 * i + 1) mine = y;
                         }
-                        if (lane < 8) gmax[quad * HG + 8 * c + lane] = mine;
                     }
+                    if (lane < HG) gmax[quad * HG + lane] = mine;
                     bar_sync_n(3 + 2 * hg, 128);
-                    float f = 1.f;
-                    if (lane < HG && ((eights >> (lane >> 3)) & 1u)) {
+                    float by = 0.f;   // how far a lane's head goes up
+                    if (lane < HG) {
                         const float tm = fmaxf(fmaxf(gmax[lane], gmax[HG + lane]), fmaxf(gmax[2 * HG + lane], gmax[3 * HG + lane]));
-                        if (tm > m + kRaise) {
-                            f = ex2f(m - (tm - kTop));
-                            m = tm - kTop;
+                        if (tm > kRaise) {
+                            by = tm - kTop;
+                            m += by;
                             negm[lane] = -m;
                         }
                     }
-                    __syncwarp();
-                    tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < HG / 8; ++c) {
                         if (!((eights >> c) & 1u)) continue;
-                        uint32_t u[8];
-                        tmem_ld_x8(s_t + 8 * c, u);
-                        tmem_ld_wait();
+                        float fc[8];   // what the row's earlier tiles made of these heads shrinks
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            e[4 * c + i] = fma2(pku(u[2 * i], u[2 * i + 1]), c2,
-                                                add2(lv2, *reinterpret_cast<const f2 *>(negm + 8 * c + 2 * i)));
-                        if (t > i0) {   // what the row's earlier tiles made of these heads shrinks
-                            float fc[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) fc[k] = __shfl_sync(0xffffffffu, f, 8 * c + k);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) l[4 * c + i] = fma2(l[4 * c + i], pk(fc[2 * i], fc[2 * i + 1]), 0);
+                        for (int i = 0; i < 4; ++i) {
+                            const float b0 = __shfl_sync(0xffffffffu, by, 8 * c + 2 * i);
+                            const float b1 = __shfl_sync(0xffffffffu, by, 8 * c + 2 * i + 1);
+                            fc[2 * i] = ex2f(-b0);
+                            fc[2 * i + 1] = ex2f(-b1);
+                            e[4 * c + i] = add2(e[4 * c + i], pk(-b0, -b1));
+                            l[4 * c + i] = fma2(l[4 * c + i], pk(fc[2 * i], fc[2 * i + 1]), 0);
+                        }
+                        if (t > i0) {
 #pragma unroll
                             for (int part = 0; part < 2; ++part) {
                                 uint32_t o[8];
@@ -659,11 +668,11 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                         }
                     }
                     tmem_st_wait_all();
+                    __syncwarp();
                 }
                 // P^T as an MN-major operand without swizzle: 16-byte rows of 16 heads, the
                 // rows of 8 keys 16 bytes apart, the head chunks of a key group 128 bytes
                 // apart (first all high parts, then the low ones), key groups N2 * 8 bytes apart
-                uint8_t *pbuf = pbuf0 + ((t - i0) & 1) * C::kP;
 #pragma unroll
                 for (int c = 0; c < HG / 16; ++c) {
                     uint32_t hi[4], lo[4];
@@ -693,7 +702,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     break;
                 }
             }
-            bar_sync_n(kBarFirst, C::kThreads - 96);   // P V of the last tile is done
+            bar_sync_n(kBarSoft, kSoft);   // P V of the last tile is done
             tc_fence_after();
 
             // the row's sums over this warp's keys, each step on half as many heads as the
