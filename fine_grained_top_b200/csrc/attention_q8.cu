@@ -47,7 +47,8 @@ namespace sa {
 namespace {
 
 constexpr int kTile = 128;                  // keys per tile (MMA M)
-constexpr float kTop = 1.f, kRaise = 8.75f; // log2 of the largest P after a raise, and before the next
+constexpr float kTop = 1.f, kRaise = 8.75f; // log2 of a row's largest P at first, and of what it may grow to
+constexpr float kStep = 8.f;                // how far a head's reference goes up then
 constexpr float kLowest = -1e30f;           // running maximum of a row that has met no key yet
 constexpr int kSmemSm = 233472;             // shared memory of an SM, 1 KB of it reserved per CTA
 
@@ -67,8 +68,15 @@ struct Cfg {
     static constexpr int kThreads = 128 + 128 * NG;       // loader warps, softmax warps
     static constexpr int kKV = kTile * D, kQ = N2 * D, kP = kTile * N2;
     static constexpr int kOffK = 0;
-    static constexpr int kOffV = kOffK + 2 * kKV;                     // two K tiles, two V tiles
-    static constexpr int kOffQ = kOffV + 2 * kKV;
+    // K and V tiles: two each with 64 heads (two CTAs an SM at most anyway), one each
+    // with fewer (more CTAs instead: 16 heads, 2048 rows of 9 tiles: 142 us with two)
+    static constexpr int ST = HQP == 64 ? 2 : 1;
+    // Q's parts: one after the other into the same columns of S, or with 16 heads side
+    // by side (half the MMAs, which are all of the least size, for one more addition)
+    static constexpr bool kSide = HQP == 16;
+    static constexpr int SN = kSide ? N2 : HQP;           // columns of an S buffer
+    static constexpr int kOffV = kOffK + ST * kKV;
+    static constexpr int kOffQ = kOffV + ST * kKV;
     static constexpr int kOffP = kOffQ + kQ;
     static constexpr int kOffRows = kOffP + kP;                   // [4][128] cache rows of a tile's keys
     static constexpr int kOffSc = kOffRows + 4 * kTile * 4;           // [2][3][128] score factor, log2 vs, 1 / vs
@@ -79,7 +87,7 @@ struct Cfg {
     static constexpr int kOffFlags = kOffMerge + 2 * (HQP + 16) * 4;  // [group][4] heads to raise, by eights
     static constexpr int kOffMisc = kOffFlags + NG * 16;
     static constexpr int kUsed = kOffMisc + 64;
-    static constexpr uint32_t kTmemCols = 2 * HQP + N2;               // two S buffers, O
+    static constexpr uint32_t kTmemCols = 2 * SN + N2 <= 64 ? 64 : (2 * SN + N2 <= 128 ? 128 : 256);   // two S buffers, O
     // CTAs wait for TMEM columns while others of their cluster wait for them, so
     // whatever shares an SM must fit its 512 columns: shared memory in proportion.
     static constexpr int kLeast = (int)(kTmemCols * (kSmemSm / 512)) - 1024;
@@ -91,7 +99,7 @@ struct Cfg {
     static_assert(kRegsLoad * 128 + kRegsSoft * 128 * NG <= kRegs * kThreads, "registers of the launch");
     static_assert(kRegs * kThreads * kByRegs <= 65536, "registers of an SM");
     static constexpr int kPerSm = kSmemSm / (kSmem + 1024) < kByRegs ? kSmemSm / (kSmem + 1024) : kByRegs;
-    static_assert(4 * kKV >= HQP * D * 4, "the partial O of a cluster's CTA lies in the K and V tiles");
+    static_assert(2 * ST * kKV >= HQP * D * 4, "the partial O of a cluster's CTA lies in the K and V tiles");
 };
 
 // ------------------------------------------------------------------ helpers
@@ -125,18 +133,8 @@ template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
-          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-}
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[8]) { tmem_ld_x8(taddr, r); }
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_x16(taddr, r); }
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_x32(taddr, r); }
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
     asm volatile("{ .reg .pred p; .reg .b32 d; elect.sync d|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
@@ -231,7 +229,7 @@ __device__ __forceinline__ uint64_t desc_v(uint32_t addr) {
 template <int D, int HQP>
 __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) attn_q8_kernel(Params P) {
     using C = Cfg<D, HQP>;
-    constexpr int N2 = C::N2, NT = C::kThreads, HG = C::HG;
+    constexpr int N2 = C::N2, NT = C::kThreads, HG = C::HG, SN = C::SN, ST = C::ST;
     extern __shared__ __align__(1024) uint8_t sm[];   // (no static shared memory: it begins 1024-byte aligned)
     int32_t *rows = reinterpret_cast<int32_t *>(sm + C::kOffRows);
     float *sc = reinterpret_cast<float *>(sm + C::kOffSc);
@@ -281,7 +279,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);   // S buffers (HQP columns each), O (N2 columns)
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);   // two S buffers (SN columns each), O (N2 columns)
 
     int p = nv - 1;
     if (nv < 0 || nv > A.S_max) {
@@ -416,7 +414,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
 #pragma unroll
             for (int i = 1; i < NIT; ++i) a = min(a, ids[i]);
             const uint8_t *from = src + (tid % CPH) * 16;
-            uint8_t *to = sm + off + ((t - i0) & 1) * C::kKV + sw<D>(tid / CPH, tid % CPH);   // RPT is a multiple of 8: one swizzle for all rows
+            uint8_t *to = sm + off + (ST == 2 ? ((t - i0) & 1) * C::kKV : 0) + sw<D>(tid / CPH, tid % CPH);   // RPT is a multiple of 8: one swizzle for all rows
             if (__all_sync(0xffffffffu, a >= 0)) {
 #pragma unroll
                 for (int i = 0; i < NIT; ++i) cp_async16(to + i * RPT * D, from + (int64_t)ids[i] * D);
@@ -429,7 +427,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         if (loader) {
             gather(i0, A.k, C::kOffK);
             gather(i0, A.v, C::kOffV);
-            if (i0 + 1 < i1) gather(i0 + 1, A.k, C::kOffK);
+            if (ST == 2 && i0 + 1 < i1) gather(i0 + 1, A.k, C::kOffK);
         }
         // both parts of this thread's chunks of Q, while the copies fly (heads >= Hq are zeros)
 #pragma unroll
@@ -464,12 +462,12 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         __syncthreads();
 
         auto issue_s = [&](int t) {   // both parts of Q into the same columns
-            constexpr uint32_t idesc = idesc_e4m3_f32(128, HQP);
-            const uint64_t kd = smem_desc(smem_u32(sm + C::kOffK + ((t - i0) & 1) * C::kKV), 8 * D, D == 128 ? 2 : 4);
+            constexpr uint32_t idesc = idesc_e4m3_f32(128, SN);
+            const uint64_t kd = smem_desc(smem_u32(sm + C::kOffK + (ST == 2 ? ((t - i0) & 1) * C::kKV : 0)), 8 * D, D == 128 ? 2 : 4);
             const uint64_t qd = smem_desc(smem_u32(sm + C::kOffQ), 8 * D, D == 128 ? 2 : 4);
-            const uint32_t dt = tmem + (uint32_t)(((t - i0) & 1) * HQP);
+            const uint32_t dt = tmem + (uint32_t)(((t - i0) & 1) * SN);
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
+            for (int part = 0; part < (C::kSide ? 1 : 2); ++part)
 #pragma unroll
                 for (int kk = 0; kk < D / 32; ++kk)
                     tc_mma_f8(dt, kd + (uint64_t)((kk * 32) >> 4), qd + (uint64_t)((part * HQP * D + kk * 32) >> 4), idesc,
@@ -478,17 +476,17 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         };
         auto issue_pv = [&](int t) {   // A (V^T) and B (P^T) both MN-major
             constexpr uint32_t idesc = idesc_e4m3_f32(128, N2) | (1u << 15) | (1u << 16);
-            const uint64_t vd = desc_v<D>(smem_u32(sm + C::kOffV + ((t - i0) & 1) * C::kKV));
+            const uint64_t vd = desc_v<D>(smem_u32(sm + C::kOffV + (ST == 2 ? ((t - i0) & 1) * C::kKV : 0)));
             const uint64_t pd = desc_mn_plain(smem_u32(sm + C::kOffP), N2 * 8, 128);
 #pragma unroll
             for (int kk = 0; kk < kTile / 32; ++kk)   // 32 keys: four 8-key groups
-                tc_mma_f8(tmem + 2 * HQP, vd + (uint64_t)((kk * 32 * D) >> 4), pd + (uint64_t)((kk * 4 * N2 * 8) >> 4), idesc,
+                tc_mma_f8(tmem + 2 * SN, vd + (uint64_t)((kk * 32 * D) >> 4), pd + (uint64_t)((kk * 4 * N2 * 8) >> 4), idesc,
                           (t == i0 && kk == 0) ? 0u : 1u);
             tc_commit(bar_pv);
         };
         if (warp == 0 && elect_one()) {
             issue_s(i0);
-            if (i0 + 1 < i1) issue_s(i0 + 1);
+            if (ST == 2 && i0 + 1 < i1) issue_s(i0 + 1);
         }
         __syncwarp();
         bool ok = true;
@@ -502,6 +500,16 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         if (loader) {
             // ------------------------------------------------------------ loader warps
             regs_dec<C::kRegsLoad>();
+            if (ST == 1 && i0 + 1 < i1) {
+                if (warp == 0) ok = wait_s(i0);   // the K tile is free
+                bar_sync_n(kBarLoad, 128);
+                gather(i0 + 1, A.k, C::kOffK);
+                cp_async_wait_all();
+                fence_async_smem();
+                bar_sync_n(kBarLoad, 128);
+                if (warp == 0 && elect_one()) issue_s(i0 + 1);
+                __syncwarp();
+            }
             for (int t = i0; t < i1; ++t) {
                 // the scores of the first tile, or P V(t - 1): O and the P tile are free for the softmax
                 if (warp == 0) {
@@ -516,18 +524,22 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     vs1 = __ldg(A.v_scale + (row1 >> P.sb_shift));
                 }
                 const int pos4 = position(t + 4);
-                // the K tile t + 2 replaces is done with (S(t)), and the V tile t + 1 replaces (P V(t - 1))
+                // two tiles: copy K(t + 2) over K(t) and V(t + 1) over V(t - 1); one: K(t + 2)
+                // over K(t + 1) and V(t) over V(t - 1)
+                if (ST == 1 && warp == 0 && t + 1 < i1) ok = ok && wait_s(t + 1);
                 bar_sync_n(kBarLoad, 128);
                 if (t + 2 < i1) gather(t + 2, A.k, C::kOffK);
-                if (t + 1 < i1) {
+                if (ST == 1) {
+                    if (t > i0) gather(t, A.v, C::kOffV);
+                } else if (t + 1 < i1) {
                     gather(t + 1, A.v, C::kOffV);
-                    put_scale(t + 1, row1, ks1, vs1);
                 }
+                if (t + 1 < i1) put_scale(t + 1, row1, ks1, vs1);
                 put_row(t + 3, pos3, pg3);
                 pos3 = pos4;
                 cp_async_wait_all();
                 fence_async_smem();
-                if (warp == 0 && t + 1 < i1) ok = ok && wait_s(t + 1);   // the softmax of t + 1 has its scores
+                if (ST == 2 && warp == 0 && t + 1 < i1) ok = ok && wait_s(t + 1);   // the softmax of t + 1 has its scores
                 if (__syncthreads_or(!ok)) {   // a wait ran out
                     ok = false;
                     break;
@@ -561,109 +573,127 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             for (int t = i0; t < i1; ++t) {
                 // S(t) is done: loader warp 0 has waited for it
                 tc_fence_after();
-                const uint32_t s_t = lane_t + (uint32_t)(((t - i0) & 1) * HQP);
+                const uint32_t s_t = lane_t + (uint32_t)(((t - i0) & 1) * SN);
                 const float *kf = sc + (t & 1) * 3 * kTile + key;
                 const f2 c2 = pk(kf[0], kf[0]), lv2 = pk(kf[kTile], kf[kTile]), iv2 = pk(kf[2 * kTile], kf[2 * kTile]);
-                uint32_t u[HG];
-                tmem_ld_cols(s_t, u);
-                tmem_ld_wait();
-                if (fresh) {
-                    // the row's first keys: their exact maxima, so that the largest P is 2
+                // Scores of N heads with the value's scale, in log2.  They are read from TMEM
+                // for the vote and again for P: keeping 32 of them beside 32 sums spills.
+                auto scores = [&](int c, auto &x) {
+                    constexpr int N = 2 * sizeof(x) / sizeof(f2);
+                    uint32_t u[N], v[N];
+                    tmem_ld_cols(s_t + (uint32_t)c, u);
+                    if (C::kSide) tmem_ld_cols(s_t + (uint32_t)(HQP + c), v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < N / 2; ++i) {
+                        x[i] = pku(u[2 * i], u[2 * i + 1]);
+                        if (C::kSide) x[i] = add2(x[i], pku(v[2 * i], v[2 * i + 1]));
+                    }
+                };
+                // e: log2 of P
+                auto exponents = [&](int c, auto &x) {
+                    constexpr int N = 2 * sizeof(x) / sizeof(f2);
+                    scores(c, x);
+#pragma unroll
+                    for (int i = 0; i < N / 4; ++i) {
+                        const ulonglong2 n2 = reinterpret_cast<const ulonglong2 *>(negm + c)[i];
+                        x[2 * i] = fma2(x[2 * i], c2, add2(lv2, n2.x));
+                        x[2 * i + 1] = fma2(x[2 * i + 1], c2, add2(lv2, n2.y));
+                    }
+                };
+                // the exact maxima over the tile's keys, a head a lane
+                auto maxima = [&]() {
                     float tm = -CUDART_INF_F;
 #pragma unroll
-                    for (int i = 0; i < HG / 2; ++i) {
-                        const float2 f = up(fma2(pku(u[2 * i], u[2 * i + 1]), c2, lv2));
-                        const float x = redux_max(f.x), y = redux_max(f.y);
-                        if (lane == 2 * i) tm = x;
-                        if (lane == 2 * i + 1) tm = y;
+                    for (int c = 0; c < HG; c += 8) {
+                        f2 x[4];
+                        scores(c, x);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 f = up(fma2(x[i], c2, lv2));
+                            const float a = redux_max(f.x), b = redux_max(f.y);
+                            if (lane == c + 2 * i) tm = a;
+                            if (lane == c + 2 * i + 1) tm = b;
+                        }
                     }
                     if (lane < HG) gmax[quad * HG + lane] = tm;
-                    fresh = !bar_or(3 + 2 * hg, 128, kf[kTile] > -CUDART_INF_F);   // (only bad pages so far)
+                    const bool any_key = bar_or(3 + 2 * hg, 128, kf[kTile] > -CUDART_INF_F);
+                    if (lane < HG) tm = fmaxf(fmaxf(gmax[lane], gmax[HG + lane]), fmaxf(gmax[2 * HG + lane], gmax[3 * HG + lane]));
+                    fresh = fresh && !any_key;
+                    return tm;
+                };
+                if (fresh) {   // the row's first keys: references by which the largest P is 2
+                    const float tm = maxima();
                     if (lane < HG) {
-                        tm = fmaxf(fmaxf(gmax[lane], gmax[HG + lane]), fmaxf(gmax[2 * HG + lane], gmax[3 * HG + lane]));
                         if (tm > kLowest) m = tm - kTop;
                         negm[lane] = -m;
                     }
                     __syncwarp();
                 }
-                // e: log2 of P
-                f2 e[HG / 2];
-                float top[HG / 8];   // the largest of each 8 heads
+                // One vote of the group a tile: does any head need a new reference?
+                float top = -CUDART_INF_F;
 #pragma unroll
-                for (int c = 0; c < HG / 8; ++c) {
-                    const ulonglong2 n0 = reinterpret_cast<const ulonglong2 *>(negm + 8 * c)[0];
-                    const ulonglong2 n1 = reinterpret_cast<const ulonglong2 *>(negm + 8 * c)[1];
-                    const f2 nm[4] = {n0.x, n0.y, n1.x, n1.y};
-                    top[c] = -CUDART_INF_F;
+                for (int c = 0; c < HG; c += 16) {
+                    f2 e[8];
+                    exponents(c, e);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        e[4 * c + i] = fma2(pku(u[8 * c + 2 * i], u[8 * c + 2 * i + 1]), c2, add2(lv2, nm[i]));
-                        const float2 f = up(e[4 * c + i]);
-                        top[c] = max3(top[c], f.x, f.y);
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 f = up(e[i]);
+                        top = max3(top, f.x, f.y);
                     }
                 }
-                float all = top[0];
-#pragma unroll
-                for (int c = 1; c < HG / 8; ++c) all = fmaxf(all, top[c]);
-                // One vote of the group a tile: does any head need a new maximum?
-                const bool raise = bar_or(2 + 2 * hg, 128, all > kRaise);
+                const bool raise = bar_or(2 + 2 * hg, 128, top > kRaise);
                 if (t > i0) bar_sync_n(kBarSoft, kSoft);   // P V(t - 1) is done: O is whole, the P tile is free
+                tc_fence_after();
                 if (raise) {
-                    // which heads, by eights; their exact maxima over the tile's keys
-                    tc_fence_after();
-                    uint32_t eights = 0;
+                    uint32_t heads = 0;   // those with an e above kRaise, for any key of the tile
+                    if (__any_sync(0xffffffffu, top > kRaise)) {
 #pragma unroll
-                    for (int c = 0; c < HG / 8; ++c) eights |= top[c] > kRaise ? 1u << c : 0u;
-                    eights = __reduce_or_sync(0xffffffffu, eights);
-                    if (lane == 0) flags[quad] = eights;
-                    bar_sync_n(3 + 2 * hg, 128);
+                        for (int c = 0; c < HG; c += 8) {
+                            f2 e[4];
+                            exponents(c, e);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 f = up(e[i]);
+                                if (f.x > kRaise) heads |= 1u << (c + 2 * i);
+                                if (f.y > kRaise) heads |= 2u << (c + 2 * i);
+                            }
+                        }
+                        heads = __reduce_or_sync(0xffffffffu, heads);
+                    }
+                    if (lane == 0) flags[quad] = heads;
+                    // They go up by kStep: nothing but a bit a head has to be known of the other
+                    // keys.  Where that is not enough, by what takes the largest P back to 2.
+                    const bool far = bar_or(3 + 2 * hg, 128, top > kRaise + kStep);
                     const uint4 fl = *reinterpret_cast<const uint4 *>(flags);
-                    eights = fl.x | fl.y | fl.z | fl.w;
-                    float mine = -CUDART_INF_F;
-#pragma unroll
-                    for (int c = 0; c < HG / 8; ++c) {
-                        if (!((eights >> c) & 1u)) continue;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 f = up(e[4 * c + i]);
-                            const float x = redux_max(f.x), y = redux_max(f.y);
-                            if (lane == 8 * c + 2 * i) mine = x;
-                            if (lane == 8 * c + 2 * i + 1) mine = y;
-                        }
+                    heads = fl.x | fl.y | fl.z | fl.w;
+                    const bool mine = (heads >> lane) & 1u;
+                    float by = mine ? kStep : 0.f;
+                    if (far) {
+                        const float tm = maxima();
+                        if (mine) by = tm - kTop - m;
                     }
-                    if (lane < HG) gmax[quad * HG + lane] = mine;
-                    bar_sync_n(3 + 2 * hg, 128);
-                    float by = 0.f;   // how far a lane's head goes up
-                    if (lane < HG) {
-                        const float tm = fmaxf(fmaxf(gmax[lane], gmax[HG + lane]), fmaxf(gmax[2 * HG + lane], gmax[3 * HG + lane]));
-                        if (tm > kRaise) {
-                            by = tm - kTop;
-                            m += by;
-                            negm[lane] = -m;
-                        }
+                    if (mine) {
+                        m += by;
+                        negm[lane] = -m;
                     }
 #pragma unroll
-                    for (int c = 0; c < HG / 8; ++c) {
-                        if (!((eights >> c) & 1u)) continue;
+                    for (int c = 0; c < HG; c += 8) {
+                        if (!((heads >> c) & 0xFFu)) continue;
                         float fc[8];   // what the row's earlier tiles made of these heads shrinks
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float b0 = __shfl_sync(0xffffffffu, by, 8 * c + 2 * i);
-                            const float b1 = __shfl_sync(0xffffffffu, by, 8 * c + 2 * i + 1);
-                            fc[2 * i] = ex2f(-b0);
-                            fc[2 * i + 1] = ex2f(-b1);
-                            e[4 * c + i] = add2(e[4 * c + i], pk(-b0, -b1));
-                            l[4 * c + i] = fma2(l[4 * c + i], pk(fc[2 * i], fc[2 * i + 1]), 0);
-                        }
+                        for (int i = 0; i < 8; ++i) fc[i] = ex2f(-__shfl_sync(0xffffffffu, by, c + i));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) l[c / 2 + i] = fma2(l[c / 2 + i], pk(fc[2 * i], fc[2 * i + 1]), 0);
                         if (t > i0) {
 #pragma unroll
                             for (int part = 0; part < 2; ++part) {
                                 uint32_t o[8];
-                                tmem_ld_x8(lane_t + (uint32_t)(2 * HQP + part * HQP + 8 * c), o);
+                                tmem_ld_x8(lane_t + (uint32_t)(2 * SN + part * HQP + c), o);
                                 tmem_ld_wait();
 #pragma unroll
                                 for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fc[k]);
-                                tmem_st8(lane_t + (uint32_t)(2 * HQP + part * HQP + 8 * c), o);
+                                tmem_st8(lane_t + (uint32_t)(2 * SN + part * HQP + c), o);
                             }
                         }
                     }
@@ -674,16 +704,18 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 // rows of 8 keys 16 bytes apart, the head chunks of a key group 128 bytes
                 // apart (first all high parts, then the low ones), key groups N2 * 8 bytes apart
 #pragma unroll
-                for (int c = 0; c < HG / 16; ++c) {
+                for (int c = 0; c < HG; c += 16) {
+                    f2 e[8];
+                    exponents(c, e);
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {   // four heads
                         uint32_t p16[2], h16[2];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const float2 f = up(e[8 * c + 2 * i + k]);
+                            const float2 f = up(e[2 * i + k]);
                             const float p0 = ex2f(f.x), p1 = ex2f(f.y);
-                            f2 &sum = l[8 * c + 2 * i + k];
+                            f2 &sum = l[c / 2 + 2 * i + k];
                             sum = fma2(pk(p0, p1), iv2, sum);
                             p16[k] = f16x2(p0, p1);
                         }
@@ -692,8 +724,8 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                         // the rest (exact) times 16
                         lo[i] = e4m3x4_of_f16(hmul2(hsub2(p16[0], h16[0]), 0x4C004C00u), hmul2(hsub2(p16[1], h16[1]), 0x4C004C00u));
                     }
-                    *reinterpret_cast<uint4 *>(pbuf + c * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(pbuf + (HQP / 16 + c) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    *reinterpret_cast<uint4 *>(pbuf + c * 8) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(pbuf + (HQP + c) * 8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 fence_async_smem();
                 tc_fence_before();
@@ -742,8 +774,8 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
 #pragma unroll
             for (int c = 0; c < HG; c += 8) {
                 uint32_t u[8], v[8];
-                tmem_ld_x8(lane_t + (uint32_t)(2 * HQP + c), u);
-                tmem_ld_x8(lane_t + (uint32_t)(3 * HQP + c), v);
+                tmem_ld_x8(lane_t + (uint32_t)(2 * SN + c), u);
+                tmem_ld_x8(lane_t + (uint32_t)(2 * SN + HQP + c), v);
                 tmem_ld_wait();
                 if (D == 128 || key < D) {
 #pragma unroll
