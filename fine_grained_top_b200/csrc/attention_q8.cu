@@ -68,23 +68,19 @@ struct Cfg {
     static constexpr int kThreads = 128 + 128 * NG;       // loader warps, softmax warps
     static constexpr int kKV = kTile * D, kQ = N2 * D, kP = kTile * N2;
     static constexpr int kOffK = 0;
-    // K and V tiles: two each with 64 heads (two CTAs an SM at most anyway), one each
-    // with fewer (more CTAs instead: 16 heads, 2048 rows of 9 tiles: 142 us with two)
-    static constexpr int ST = HQP == 64 ? 2 : 1;
     // Q's parts: one after the other into the same columns of S, or with 16 heads side
     // by side (half the MMAs, which are all of the least size, for one more addition)
     static constexpr bool kSide = HQP == 16;
     static constexpr int SN = kSide ? N2 : HQP;           // columns of an S buffer
-    static constexpr int kOffV = kOffK + ST * kKV;
-    static constexpr int kOffQ = kOffV + ST * kKV;
+    static constexpr int kOffV = kOffK + kKV;
+    static constexpr int kOffQ = kOffV + kKV;
     static constexpr int kOffP = kOffQ + kQ;
     static constexpr int kOffRows = kOffP + kP;                   // [4][128] cache rows of a tile's keys
     static constexpr int kOffSc = kOffRows + 4 * kTile * 4;           // [2][3][128] score factor, log2 vs, 1 / vs
     static constexpr int kOffMax = kOffSc + 2 * 3 * kTile * 4;           // [4][HQP] maxima or sums of the quads
     static constexpr int kOffNegM = kOffMax + 4 * HQP * 4;            // [softmax warp][HG] minus the running maxima
-    static constexpr int kOffEpi = kOffNegM + 4 * HQP * 4;            // m, l [2][HQP]
-    static constexpr int kOffMerge = kOffEpi + 2 * HQP * 4;           // [2][HQP + 16] m, l of every CTA (clusters)
-    static constexpr int kOffFlags = kOffMerge + 2 * (HQP + 16) * 4;  // [group][4] heads to raise, by eights
+    static constexpr int kOffEpi = kOffNegM + 4 * HQP * 4;            // 1 / l, or a part's m and l [2][HQP]
+    static constexpr int kOffFlags = kOffEpi + 2 * HQP * 4;  // [group][4] heads to raise, by eights
     static constexpr int kOffMisc = kOffFlags + NG * 16;
     static constexpr int kUsed = kOffMisc + 64;
     static constexpr uint32_t kTmemCols = 2 * SN + N2 <= 64 ? 64 : (2 * SN + N2 <= 128 ? 128 : 256);   // two S buffers, O
@@ -99,7 +95,7 @@ struct Cfg {
     static_assert(kRegsLoad * 128 + kRegsSoft * 128 * NG <= kRegs * kThreads, "registers of the launch");
     static_assert(kRegs * kThreads * kByRegs <= 65536, "registers of an SM");
     static constexpr int kPerSm = kSmemSm / (kSmem + 1024) < kByRegs ? kSmemSm / (kSmem + 1024) : kByRegs;
-    static_assert(2 * ST * kKV >= HQP * D * 4, "the partial O of a cluster's CTA lies in the K and V tiles");
+    static_assert(2 * kKV >= HQP * D * 4, "O lies in the K and V tiles when a row or its part is done");
 };
 
 // ------------------------------------------------------------------ helpers
@@ -226,14 +222,16 @@ __device__ __forceinline__ uint64_t desc_v(uint32_t addr) {
     return d;
 }
 
-template <int D, int HQP>
+// CL: a cluster shares the row (the two forms are apart to keep the code, and the
+// instruction cache it needs, small).
+template <int D, int HQP, bool CL>
 __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) attn_q8_kernel(Params P) {
     using C = Cfg<D, HQP>;
-    constexpr int N2 = C::N2, NT = C::kThreads, HG = C::HG, SN = C::SN, ST = C::ST;
+    constexpr int N2 = C::N2, NT = C::kThreads, HG = C::HG, SN = C::SN;
     extern __shared__ __align__(1024) uint8_t sm[];   // (no static shared memory: it begins 1024-byte aligned)
     int32_t *rows = reinterpret_cast<int32_t *>(sm + C::kOffRows);
     float *sc = reinterpret_cast<float *>(sm + C::kOffSc);
-    float *epi_m = reinterpret_cast<float *>(sm + C::kOffEpi), *epi_l = epi_m + HQP;
+    float *epi = reinterpret_cast<float *>(sm + C::kOffEpi), *epi_l = epi + HQP;   // 1 / l, or a part's m and l
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + C::kOffMisc);
     uint64_t *bar_s = bar, *bar_pv = bar + 2;   // S(t) done, one for each S buffer; P V(t) done
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 3);
@@ -242,13 +240,28 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
 
     const AttnQ8Args &A = P.a;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int rank = P.G > 1 ? (int)cluster_rank() : 0;
-    const int r = (int)blockIdx.x / P.G, b = r / A.T;
+    const int G = CL ? P.G : 1, rank = CL ? (int)cluster_rank() : 0;
+    const int r = CL ? (int)blockIdx.x / G : (int)blockIdx.x, b = r / A.T;
 
     // ------------------------------------------------------------ the row
     // What does not depend on anything goes first: its length, its Q (16 dims a
-    // thread) and its top-K.
+    // thread and turn) and the head of its top-K.
     const int nv = __ldg(A.n_valid + r);
+    const int32_t *trow = A.topk + (int64_t)r * A.K;
+    const bool vec = (A.K & 3) == 0 && (reinterpret_cast<uintptr_t>(A.topk) & 15u) == 0;
+    // entries k - 1 .. k + 3
+    auto entries = [&](int k, int (&e)[5]) {
+        e[0] = k > 0 && k < A.K ? __ldg(trow + k - 1) : -1;
+        if (vec) {
+            const int4 v = k < A.K ? __ldg(reinterpret_cast<const int4 *>(trow + k)) : make_int4(-1, -1, -1, -1);
+            e[1] = v.x; e[2] = v.y; e[3] = v.z; e[4] = v.w;
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) e[u + 1] = k + u < A.K ? __ldg(trow + k + u) : -1;
+        }
+    };
+    int first4[5];
+    entries(4 * tid, first4);
     constexpr int CPH = D / 16;   // 16-dim chunks of a head
     constexpr int NQ = (HQP * CPH + NT - 1) / NT;   // chunks a thread
     uint4 qv[2 * NQ];
@@ -275,40 +288,46 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     if (warp == 0) {
         tmem_alloc(tmem_slot, C::kTmemCols);
         tmem_relinquish();
+        __syncwarp();
+    }
+    int p = nv - 1;
+    if (nv < 0 || nv > A.S_max) {
+        if (tid == 0 && rank == 0) report(A.dev_status, SA_DEV_INDEX);
+        p = -1;
+    }
+    auto no_keys = [&]() {   // out 0, lse -infinity
+        uint4 *o = reinterpret_cast<uint4 *>(A.out + (int64_t)r * A.Hq * D);
+        for (int i = tid; i < A.Hq * D / 8; i += NT) o[i] = make_uint4(0, 0, 0, 0);
+        if (A.lse)
+            for (int i = tid; i < A.Hq; i += NT) A.lse[(int64_t)r * A.Hq + i] = -CUDART_INF_F;
+    };
+    if (p < 0 && !CL) {   // a padding row
+        no_keys();
+        if (warp == 0) tmem_dealloc(*tmem_slot, C::kTmemCols);
+        return;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);   // two S buffers (SN columns each), O (N2 columns)
 
-    int p = nv - 1;
-    if (nv < 0 || nv > A.S_max) {
-        if (tid == 0 && rank == 0) report(A.dev_status, SA_DEV_INDEX);
-        p = -1;
-    }
     const int lim = p - A.W;   // top-K entries <= lim are taken; the window covers the rest
-    const int32_t *trow = A.topk + (int64_t)r * A.K;
     if (p >= 0) {
         int first_out = A.K;
         bool bad_idx = false, bad_ord = false;
-        const bool vec = (A.K & 3) == 0 && (reinterpret_cast<uintptr_t>(A.topk) & 15u) == 0;
-#pragma unroll 2
-        for (int k = 4 * tid; k < A.K; k += 4 * NT) {
-            int e[5];
-            e[0] = k > 0 ? __ldg(trow + k - 1) : -1;
-            if (vec) {
-                const int4 v = __ldg(reinterpret_cast<const int4 *>(trow + k));
-                e[1] = v.x; e[2] = v.y; e[3] = v.z; e[4] = v.w;
-            } else {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) e[u + 1] = k + u < A.K ? __ldg(trow + k + u) : -1;
-            }
+        auto check = [&](int k, const int (&e)[5]) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 if (e[u + 1] > p) bad_idx = true;
                 if (e[u + 1] >= 0 && k + u > 0 && !(e[u] >= 0 && e[u] < e[u + 1])) bad_ord = true;
                 if (!(e[u + 1] >= 0 && e[u + 1] <= lim)) first_out = min(first_out, k + u);
             }
+        };
+        check(4 * tid, first4);
+        for (int k = 4 * (tid + NT); k < A.K; k += 4 * NT) {
+            int e[5];
+            entries(k, e);
+            check(k, e);
         }
         if (rank == 0 && bad_idx) report(A.dev_status, SA_DEV_INDEX);
         if (rank == 0 && bad_ord) report(A.dev_status, SA_DEV_ORDER);
@@ -337,13 +356,8 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     const int w0 = max(0, p - A.W + 1);
     const int n_keys = p >= 0 ? n_top + (p - w0 + 1) : 0;
     const int n_tiles = (n_keys + kTile - 1) / kTile;
-    const int i0 = (int)((int64_t)n_tiles * rank / P.G), i1 = (int)((int64_t)n_tiles * (rank + 1) / P.G);
-    if (n_keys == 0 && rank == 0) {   // no keys: out 0, lse -infinity
-        uint4 *o = reinterpret_cast<uint4 *>(A.out + (int64_t)r * A.Hq * D);
-        for (int i = tid; i < A.Hq * D / 8; i += NT) o[i] = make_uint4(0, 0, 0, 0);
-        if (A.lse)
-            for (int i = tid; i < A.Hq; i += NT) A.lse[(int64_t)r * A.Hq + i] = -CUDART_INF_F;
-    }
+    const int i0 = (int)((int64_t)n_tiles * rank / G), i1 = (int)((int64_t)n_tiles * (rank + 1) / G);
+    if (n_keys == 0 && rank == 0) no_keys();
 
     const bool loader = warp < 4;
     // softmax warps: TMEM lane quadrant, group, first head
@@ -392,15 +406,8 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             const int pg0 = page_of(pos0), pg1 = page_of(pos1), pg2 = page_of(pos2);
             pos3 = position(i0 + 3);
             put_row(i0, pos0, pg0);
-            const int row0 = row_of(i0);
-            float ks = 0.f, vs = 0.f;
-            if (row0 >= 0) {
-                ks = __ldg(A.k_scale + (row0 >> P.sb_shift));
-                vs = __ldg(A.v_scale + (row0 >> P.sb_shift));
-            }
             put_row(i0 + 1, pos1, pg1);
             put_row(i0 + 2, pos2, pg2);
-            put_scale(i0, row0, ks, vs);
         }
         __syncthreads();
 
@@ -414,7 +421,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
 #pragma unroll
             for (int i = 1; i < NIT; ++i) a = min(a, ids[i]);
             const uint8_t *from = src + (tid % CPH) * 16;
-            uint8_t *to = sm + off + (ST == 2 ? ((t - i0) & 1) * C::kKV : 0) + sw<D>(tid / CPH, tid % CPH);   // RPT is a multiple of 8: one swizzle for all rows
+            uint8_t *to = sm + off + sw<D>(tid / CPH, tid % CPH);   // RPT is a multiple of 8: one swizzle for all rows
             if (__all_sync(0xffffffffu, a >= 0)) {
 #pragma unroll
                 for (int i = 0; i < NIT; ++i) cp_async16(to + i * RPT * D, from + (int64_t)ids[i] * D);
@@ -427,7 +434,13 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         if (loader) {
             gather(i0, A.k, C::kOffK);
             gather(i0, A.v, C::kOffV);
-            if (ST == 2 && i0 + 1 < i1) gather(i0 + 1, A.k, C::kOffK);
+            const int row0 = row_of(i0);
+            float ks = 0.f, vs = 0.f;
+            if (row0 >= 0) {
+                ks = __ldg(A.k_scale + (row0 >> P.sb_shift));
+                vs = __ldg(A.v_scale + (row0 >> P.sb_shift));
+            }
+            put_scale(i0, row0, ks, vs);
         }
         // both parts of this thread's chunks of Q, while the copies fly (heads >= Hq are zeros)
 #pragma unroll
@@ -463,7 +476,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
 
         auto issue_s = [&](int t) {   // both parts of Q into the same columns
             constexpr uint32_t idesc = idesc_e4m3_f32(128, SN);
-            const uint64_t kd = smem_desc(smem_u32(sm + C::kOffK + (ST == 2 ? ((t - i0) & 1) * C::kKV : 0)), 8 * D, D == 128 ? 2 : 4);
+            const uint64_t kd = smem_desc(smem_u32(sm + C::kOffK), 8 * D, D == 128 ? 2 : 4);
             const uint64_t qd = smem_desc(smem_u32(sm + C::kOffQ), 8 * D, D == 128 ? 2 : 4);
             const uint32_t dt = tmem + (uint32_t)(((t - i0) & 1) * SN);
 #pragma unroll
@@ -476,7 +489,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         };
         auto issue_pv = [&](int t) {   // A (V^T) and B (P^T) both MN-major
             constexpr uint32_t idesc = idesc_e4m3_f32(128, N2) | (1u << 15) | (1u << 16);
-            const uint64_t vd = desc_v<D>(smem_u32(sm + C::kOffV + (ST == 2 ? ((t - i0) & 1) * C::kKV : 0)));
+            const uint64_t vd = desc_v<D>(smem_u32(sm + C::kOffV));
             const uint64_t pd = desc_mn_plain(smem_u32(sm + C::kOffP), N2 * 8, 128);
 #pragma unroll
             for (int kk = 0; kk < kTile / 32; ++kk)   // 32 keys: four 8-key groups
@@ -484,10 +497,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                           (t == i0 && kk == 0) ? 0u : 1u);
             tc_commit(bar_pv);
         };
-        if (warp == 0 && elect_one()) {
-            issue_s(i0);
-            if (ST == 2 && i0 + 1 < i1) issue_s(i0 + 1);
-        }
+        if (warp == 0 && elect_one()) issue_s(i0);
         __syncwarp();
         bool ok = true;
         // P V(t) is phase t - i0 of its barrier; S(t) may end while some warp still looks for
@@ -500,7 +510,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         if (loader) {
             // ------------------------------------------------------------ loader warps
             regs_dec<C::kRegsLoad>();
-            if (ST == 1 && i0 + 1 < i1) {
+            if (i0 + 1 < i1) {
                 if (warp == 0) ok = wait_s(i0);   // the K tile is free
                 bar_sync_n(kBarLoad, 128);
                 gather(i0 + 1, A.k, C::kOffK);
@@ -524,22 +534,15 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     vs1 = __ldg(A.v_scale + (row1 >> P.sb_shift));
                 }
                 const int pos4 = position(t + 4);
-                // two tiles: copy K(t + 2) over K(t) and V(t + 1) over V(t - 1); one: K(t + 2)
-                // over K(t + 1) and V(t) over V(t - 1)
-                if (ST == 1 && warp == 0 && t + 1 < i1) ok = ok && wait_s(t + 1);
+                if (warp == 0 && t + 1 < i1) ok = ok && wait_s(t + 1);   // (and the softmax of t + 1 has its scores)
                 bar_sync_n(kBarLoad, 128);
-                if (t + 2 < i1) gather(t + 2, A.k, C::kOffK);
-                if (ST == 1) {
-                    if (t > i0) gather(t, A.v, C::kOffV);
-                } else if (t + 1 < i1) {
-                    gather(t + 1, A.v, C::kOffV);
-                }
+                if (t + 2 < i1) gather(t + 2, A.k, C::kOffK);   // over K(t + 1): S(t + 1) is done
+                if (t > i0) gather(t, A.v, C::kOffV);           // over V(t - 1): P V(t - 1) is done
                 if (t + 1 < i1) put_scale(t + 1, row1, ks1, vs1);
                 put_row(t + 3, pos3, pg3);
                 pos3 = pos4;
                 cp_async_wait_all();
                 fence_async_smem();
-                if (ST == 2 && warp == 0 && t + 1 < i1) ok = ok && wait_s(t + 1);   // the softmax of t + 1 has its scores
                 if (__syncthreads_or(!ok)) {   // a wait ran out
                     ok = false;
                     break;
@@ -761,16 +764,20 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             if (quad == 0 && lane < HG) {
                 const float L = (gmax[lane] + gmax[HG + lane]) + (gmax[2 * HG + lane] + gmax[3 * HG + lane]);
                 const int h = h0 + lane;
-                epi_m[h] = P.G > 1 ? m : (L == 0.f ? 0.f : 1.f / L);   // (whole rows need no m any more)
-                epi_l[h] = L;
-                if (P.G == 1 && A.lse && h < A.Hq)
-                    A.lse[(int64_t)r * A.Hq + h] = L == 0.f ? -CUDART_INF_F : (m + log2f(L)) * 0.69314718055994531f;
+                if (CL) {
+                    epi[h] = m;
+                    epi_l[h] = L;
+                } else {
+                    epi[h] = L == 0.f ? 0.f : 1.f / L;
+                    if (A.lse && h < A.Hq)
+                        A.lse[(int64_t)r * A.Hq + h] = L == 0.f ? -CUDART_INF_F : (m + log2f(L)) * 0.69314718055994531f;
+                }
             }
             bar_sync_n(3 + 2 * hg, 128);
-            // O = O_hi + O_lo / 16; a part of a row stays unnormalised, for the merge (the
-            // K and V tiles are idle by now)
-            float *part = reinterpret_cast<float *>(sm + C::kOffK);
-            uint16_t *orow = A.out + (int64_t)r * A.Hq * D;
+            // O = O_hi + O_lo / 16 into shared memory (the K and V tiles are idle by now): a part
+            // of a row as it is, for the join; a row normalised, and out in 16-byte stores
+            float *part = reinterpret_cast<float *>(sm + C::kOffK) + h0 * D;
+            uint16_t *stage = reinterpret_cast<uint16_t *>(sm + C::kOffK) + h0 * D;
 #pragma unroll
             for (int c = 0; c < HG; c += 8) {
                 uint32_t u[8], v[8];
@@ -780,21 +787,26 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 if (D == 128 || key < D) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const int h = h0 + c + k;
                         const float o = fmaf(__uint_as_float(v[k]), 0.0625f, __uint_as_float(u[k]));
-                        if (P.G > 1) {
-                            part[h * D + key] = o;
-                        } else if (h < A.Hq) {
-                            const __nv_bfloat16 ob = __float2bfloat16_rn(o * epi_m[h]);
-                            orow[(int64_t)h * D + key] = *reinterpret_cast<const uint16_t *>(&ob);
+                        if (CL) {
+                            part[(c + k) * D + key] = o;
+                        } else {
+                            const __nv_bfloat16 ob = __float2bfloat16_rn(o * epi[h0 + c + k]);
+                            stage[(c + k) * D + key] = *reinterpret_cast<const uint16_t *>(&ob);
                         }
                     }
                 }
             }
+            if (!CL) {
+                bar_sync_n(3 + 2 * hg, 128);
+                uint4 *o = reinterpret_cast<uint4 *>(A.out + ((int64_t)r * A.Hq + h0) * D);
+                const int n = min(HG, A.Hq - h0) * (D / 8);
+                for (int i = quad * 32 + lane; i < n; i += 128) o[i] = reinterpret_cast<const uint4 *>(stage)[i];
+            }
             regs_dec<C::kRegs>();
         }
-    } else if (tid < HQP) {   // no share of the row
-        epi_m[tid] = kLowest;
+    } else if (CL && tid < HQP) {   // no share of the row
+        epi[tid] = kLowest;
         epi_l[tid] = 0.f;
     }
     tc_fence_before();
@@ -803,64 +815,73 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmemCols);
     }
-    if (P.G > 1) {
-        // join the parts: this CTA takes the heads rank * hpr .., 4 dims a thread
+    if (CL) {
+        // join the parts of the heads rank * hpr ..: 4 dims a thread, four threads of which
+        // each takes every fourth part, all of its loads in flight at once
         cluster_sync();
-        const int G = P.G, hpr = (A.Hq + G - 1) / G, hb = rank * hpr, nh = n_keys > 0 ? max(0, min(hpr, A.Hq - hb)) : 0;
-        float *gm = reinterpret_cast<float *>(sm + C::kOffMerge), *gl = gm + HQP + 16;   // [head][CTA]
-        for (int i = tid; i < nh * G; i += NT) {
-            const int h = i / G, c = i % G;
-            gm[i] = dsmem_ld_f32(epi_m + hb + h, (uint32_t)c);
-            gl[i] = dsmem_ld_f32(epi_l + hb + h, (uint32_t)c);
-        }
-        __syncthreads();
+        const int hpr = (A.Hq + G - 1) / G, hb = rank * hpr, nh = n_keys > 0 ? max(0, min(hpr, A.Hq - hb)) : 0;
         const float *part = reinterpret_cast<const float *>(sm + C::kOffK);
-        for (int i = tid; i < nh * (D / 4); i += NT) {
-            const int h = i / (D / 4), d4 = i % (D / 4);
+        const int n = nh * D;
+        for (int i = tid; i < (n + 31) / 32 * 32; i += NT) {   // whole warps
+            const int ii = min(i, n - 1), cq = ii & 3, d4 = (ii >> 2) % (D / 4), h = (ii >> 2) / (D / 4);
+            float mc[4], lc[4];
+            float4 vc[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int c = cq + 4 * u;
+                mc[u] = kLowest;
+                lc[u] = 0.f;
+                if (c < G) {
+                    mc[u] = dsmem_ld_f32(epi + hb + h, (uint32_t)c);
+                    lc[u] = dsmem_ld_f32(epi_l + hb + h, (uint32_t)c);
+                    vc[u] = dsmem_ld_f4(part + (hb + h) * D + 4 * d4, (uint32_t)c);
+                }
+            }
             float m = kLowest, L = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int c = 0; c < G; ++c)
-                if (gl[h * G + c] != 0.f) m = fmaxf(m, gm[h * G + c]);
-#pragma unroll 4
-            for (int c = 0; c < G; ++c) {
-                const float lc = gl[h * G + c];
-                if (lc == 0.f) continue;   // no share of the row
-                const float f = ex2f(gm[h * G + c] - m);
-                const float4 v = dsmem_ld_f4(part + (hb + h) * D + 4 * d4, (uint32_t)c);
-                L = fmaf(f, lc, L);
-                o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (lc[u] != 0.f) m = fmaxf(m, mc[u]);
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (lc[u] == 0.f) continue;   // no share of the row (and nothing written)
+                const float f = ex2f(mc[u] - m);
+                L = fmaf(f, lc[u], L);
+                o.x = fmaf(f, vc[u].x, o.x); o.y = fmaf(f, vc[u].y, o.y);
+                o.z = fmaf(f, vc[u].z, o.z); o.w = fmaf(f, vc[u].w, o.w);
             }
-            const float s = L == 0.f ? 0.f : 1.f / L;
-            uint2 ob;
-            ob.x = pack_bf16(o.x * s, o.y * s);
-            ob.y = pack_bf16(o.z * s, o.w * s);
-            *reinterpret_cast<uint2 *>(A.out + ((int64_t)r * A.Hq + hb + h) * D + 4 * d4) = ob;
-            if (A.lse && d4 == 0)
-                A.lse[(int64_t)r * A.Hq + hb + h] = L == 0.f ? -CUDART_INF_F : (m + log2f(L)) * 0.69314718055994531f;
+#pragma unroll
+            for (int k = 1; k <= 2; k <<= 1) {
+                L += __shfl_xor_sync(0xffffffffu, L, k);
+                o.x += __shfl_xor_sync(0xffffffffu, o.x, k);
+                o.y += __shfl_xor_sync(0xffffffffu, o.y, k);
+                o.z += __shfl_xor_sync(0xffffffffu, o.z, k);
+                o.w += __shfl_xor_sync(0xffffffffu, o.w, k);
+            }
+            if (cq == 0 && i < n) {
+                const float s = L == 0.f ? 0.f : 1.f / L;
+                uint2 ob;
+                ob.x = pack_bf16(o.x * s, o.y * s);
+                ob.y = pack_bf16(o.z * s, o.w * s);
+                *reinterpret_cast<uint2 *>(A.out + ((int64_t)r * A.Hq + hb + h) * D + 4 * d4) = ob;
+                if (A.lse && d4 == 0)
+                    A.lse[(int64_t)r * A.Hq + hb + h] = L == 0.f ? -CUDART_INF_F : (m + log2f(L)) * 0.69314718055994531f;
+            }
         }
         cluster_sync();   // nobody leaves while its parts are read
     }
 }
 
-template <int D, int HQP>
-sa_status launch_q8(const AttnQ8Args &a, cudaStream_t st) {
+template <int D, int HQP, bool CL>
+sa_status launch_q8(const Params &p, int R, cudaStream_t st) {
     using C = Cfg<D, HQP>;
-    int dev = 0, sms = 148;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return SA_ERR_CUDA;
-    Params p;
-    p.a = a;
-    const int R = a.B * a.T;
-    const int tiles = (int)std::min<int64_t>(((int64_t)a.K + a.W + kTile - 1) / kTile, ((int64_t)a.S_max + kTile - 1) / kTile);
-    p.G = std::max(1, std::min({16, tiles, sms * C::kPerSm / R}));
-    p.sb_shift = 0;
-    while ((1 << p.sb_shift) < a.scale_block) ++p.sb_shift;
-    p.scale_log2 = a.scale * 1.4426950408889634f;
-    if (prepare_kernel<attn_q8_kernel<D, HQP>>(C::kSmem, p.G > 8) != cudaSuccess) return SA_ERR_CUDA;
+    if (prepare_kernel<attn_q8_kernel<D, HQP, CL>>(C::kSmem, CL) != cudaSuccess) return SA_ERR_CUDA;
     // the warps' register shares are taken from what the launch gives its threads
     static const int regs = [] {
         cudaFuncAttributes f;
-        return cudaFuncGetAttributes(&f, attn_q8_kernel<D, HQP>) == cudaSuccess ? f.numRegs : 0;
+        return cudaFuncGetAttributes(&f, attn_q8_kernel<D, HQP, CL>) == cudaSuccess ? f.numRegs : 0;
     }();
     if (regs < C::kRegs) return SA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
@@ -873,15 +894,32 @@ sa_status launch_q8(const AttnQ8Args &a, cudaStream_t st) {
     at.val.clusterDim.x = (unsigned)p.G;
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
-    cfg.numAttrs = p.G > 1 ? 1 : 0;
-    return cuda_ok(cudaLaunchKernelEx(&cfg, attn_q8_kernel<D, HQP>, p));
+    cfg.numAttrs = CL ? 1 : 0;
+    return cuda_ok(cudaLaunchKernelEx(&cfg, attn_q8_kernel<D, HQP, CL>, p));
+}
+
+template <int D, int HQP>
+sa_status launch_q8_rows(const AttnQ8Args &a, cudaStream_t st) {
+    using C = Cfg<D, HQP>;
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return SA_ERR_CUDA;
+    Params p;
+    p.a = a;
+    const int R = a.B * a.T;
+    const int tiles = (int)std::min<int64_t>(((int64_t)a.K + a.W + kTile - 1) / kTile, ((int64_t)a.S_max + kTile - 1) / kTile);
+    p.G = std::max(1, std::min({16, tiles, sms * C::kPerSm / R}));
+    p.sb_shift = 0;
+    while ((1 << p.sb_shift) < a.scale_block) ++p.sb_shift;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    return p.G > 1 ? launch_q8<D, HQP, true>(p, R, st) : launch_q8<D, HQP, false>(p, R, st);
 }
 
 template <int D>
 sa_status launch_q8_heads(const AttnQ8Args &a, cudaStream_t st) {
-    if (a.Hq <= 16) return launch_q8<D, 16>(a, st);
-    if (a.Hq <= 32) return launch_q8<D, 32>(a, st);
-    return launch_q8<D, 64>(a, st);
+    if (a.Hq <= 16) return launch_q8_rows<D, 16>(a, st);
+    if (a.Hq <= 32) return launch_q8_rows<D, 32>(a, st);
+    return launch_q8_rows<D, 64>(a, st);
 }
 
 }  // namespace
