@@ -37,6 +37,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "gather_pipe.cuh"
 #include "internal.h"
@@ -898,6 +899,36 @@ sa_status launch_q8(const Params &p, int R, cudaStream_t st) {
     return cuda_ok(cudaLaunchKernelEx(&cfg, attn_q8_kernel<D, HQP, CL>, p));
 }
 
+// How many clusters of G of these CTAs the device runs at once, one CTA an SM
+// (asked once for each device and size; clusters do not span GPCs, so it is
+// less than SMs / G: 33 of 4, 15 of 8 or 9, 11 of 10, 7 of 12 to 16 on 148 SMs).
+template <int D, int HQP>
+int active_clusters(int dev, int sms, int G) {
+    if (G == 1) return sms;
+    static std::atomic<int> known[64][17];
+    const int k = dev < 64 ? known[dev][G].load(std::memory_order_relaxed) : 0;
+    if (k > 0) return k;
+    using C = Cfg<D, HQP>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)G);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)G;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, attn_q8_kernel<D, HQP, true>, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        return 0;
+    }
+    n = std::min(n, sms / G);
+    if (dev < 64) known[dev][G].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 template <int D, int HQP>
 sa_status launch_q8_rows(const AttnQ8Args &a, cudaStream_t st) {
     using C = Cfg<D, HQP>;
@@ -908,7 +939,27 @@ sa_status launch_q8_rows(const AttnQ8Args &a, cudaStream_t st) {
     p.a = a;
     const int R = a.B * a.T;
     const int tiles = (int)std::min<int64_t>(((int64_t)a.K + a.W + kTile - 1) / kTile, ((int64_t)a.S_max + kTile - 1) / kTile);
-    p.G = std::max(1, std::min({16, tiles, sms * C::kPerSm / R}));
+    // CTAs a row.  In units of one tile's time in a cluster (1.2 us with 16 heads, 1.8
+    // with 64), alone on an SM, a cluster takes 6 for its row's start and join and 1 a
+    // tile, a single CTA 4.7 and 0.9; another CTA on the SM costs all of them 28 percent
+    // with up to 32 heads, 42 with 64 (fitted to rows of 4 to 40 tiles, 1 to 300 rows:
+    // 8 rows of 20 tiles and 64 heads 13.9 us with 10 CTAs a row, 38 with one, 18 with 16;
+    // 100 such rows 46 us with one, 50 with 4).
+    p.G = 1;
+    double best = 0;
+    if (prepare_kernel<attn_q8_kernel<D, HQP, true>>(C::kSmem, true) != cudaSuccess) return SA_ERR_CUDA;
+    for (int G = 1; G <= std::min(16, tiles); ++G) {
+        if (G > 1 && (R >= 2 * sms || (tiles + G - 1) / G == (tiles + G - 2) / (G - 1))) continue;
+        const int at_once = active_clusters<D, HQP>(dev, sms, G);
+        if (at_once < 1) continue;
+        const int n = (R + at_once - 1) / at_once, t = (tiles + G - 1) / G;
+        const double cost = (G == 1 ? 4.7 + 0.9 * t : 6.0 + t) * (1.0 + (HQP == 64 ? 0.42 : 0.28) * (std::min(n, C::kPerSm) - 1)) *
+                            ((n + C::kPerSm - 1) / C::kPerSm);
+        if (G == 1 || cost < best) {
+            best = cost;
+            p.G = G;
+        }
+    }
     p.sb_shift = 0;
     while ((1 << p.sb_shift) < a.scale_block) ++p.sb_shift;
     p.scale_log2 = a.scale * 1.4426950408889634f;
