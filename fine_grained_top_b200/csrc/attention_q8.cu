@@ -245,24 +245,10 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     const int r = CL ? (int)blockIdx.x / G : (int)blockIdx.x, b = r / A.T;
 
     // ------------------------------------------------------------ the row
-    // What does not depend on anything goes first: its length, its Q (16 dims a
-    // thread and turn) and the head of its top-K.
+    // What does not depend on anything goes first: its length and its Q (16 dims a
+    // thread and turn).
     const int nv = __ldg(A.n_valid + r);
     const int32_t *trow = A.topk + (int64_t)r * A.K;
-    const bool vec = (A.K & 3) == 0 && (reinterpret_cast<uintptr_t>(A.topk) & 15u) == 0;
-    // entries k - 1 .. k + 3
-    auto entries = [&](int k, int (&e)[5]) {
-        e[0] = k > 0 && k < A.K ? __ldg(trow + k - 1) : -1;
-        if (vec) {
-            const int4 v = k < A.K ? __ldg(reinterpret_cast<const int4 *>(trow + k)) : make_int4(-1, -1, -1, -1);
-            e[1] = v.x; e[2] = v.y; e[3] = v.z; e[4] = v.w;
-        } else {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) e[u + 1] = k + u < A.K ? __ldg(trow + k + u) : -1;
-        }
-    };
-    int first4[5];
-    entries(4 * tid, first4);
     constexpr int CPH = D / 16;   // 16-dim chunks of a head
     constexpr int NQ = (HQP * CPH + NT - 1) / NT;   // chunks a thread
     uint4 qv[2 * NQ];
@@ -316,19 +302,23 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     if (p >= 0) {
         int first_out = A.K;
         bool bad_idx = false, bad_ord = false;
-        auto check = [&](int k, const int (&e)[5]) {
+        const bool vec = (A.K & 3) == 0 && (reinterpret_cast<uintptr_t>(A.topk) & 15u) == 0;
+        for (int k = 4 * tid; k < A.K; k += 4 * NT) {
+            int e[5];   // entries k - 1 .. k + 3
+            e[0] = k > 0 ? __ldg(trow + k - 1) : -1;
+            if (vec) {
+                const int4 v = __ldg(reinterpret_cast<const int4 *>(trow + k));
+                e[1] = v.x; e[2] = v.y; e[3] = v.z; e[4] = v.w;
+            } else {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) e[u + 1] = k + u < A.K ? __ldg(trow + k + u) : -1;
+            }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 if (e[u + 1] > p) bad_idx = true;
                 if (e[u + 1] >= 0 && k + u > 0 && !(e[u] >= 0 && e[u] < e[u + 1])) bad_ord = true;
                 if (!(e[u + 1] >= 0 && e[u + 1] <= lim)) first_out = min(first_out, k + u);
             }
-        };
-        check(4 * tid, first4);
-        for (int k = 4 * (tid + NT); k < A.K; k += 4 * NT) {
-            int e[5];
-            entries(k, e);
-            check(k, e);
         }
         if (rank == 0 && bad_idx) report(A.dev_status, SA_DEV_INDEX);
         if (rank == 0 && bad_ord) report(A.dev_status, SA_DEV_ORDER);
@@ -418,30 +408,22 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
 #pragma unroll
             for (int q = 0; q < NIT / 4; ++q)
                 reinterpret_cast<int4 *>(ids)[q] = reinterpret_cast<const int4 *>(rows + (t & 3) * kTile + (tid / CPH) * NIT)[q];
-            int a = ids[0];
-#pragma unroll
-            for (int i = 1; i < NIT; ++i) a = min(a, ids[i]);
             const uint8_t *from = src + (tid % CPH) * 16;
             uint8_t *to = sm + off + sw<D>(tid / CPH, tid % CPH);   // RPT is a multiple of 8: one swizzle for all rows
-            if (__all_sync(0xffffffffu, a >= 0)) {
 #pragma unroll
-                for (int i = 0; i < NIT; ++i) cp_async16(to + i * RPT * D, from + (int64_t)ids[i] * D);
-            } else {
-#pragma unroll
-                for (int i = 0; i < NIT; ++i)
-                    cp_async16_or_zero(to + i * RPT * D, from + (int64_t)max(ids[i], 0) * D, ids[i] >= 0);
-            }
+            for (int i = 0; i < NIT; ++i)
+                cp_async16_or_zero(to + i * RPT * D, from + (int64_t)max(ids[i], 0) * D, ids[i] >= 0);
         };
+        int row0 = -1;
+        float ks0 = 0.f, vs0 = 0.f;
         if (loader) {
             gather(i0, A.k, C::kOffK);
             gather(i0, A.v, C::kOffV);
-            const int row0 = row_of(i0);
-            float ks = 0.f, vs = 0.f;
+            row0 = row_of(i0);
             if (row0 >= 0) {
-                ks = __ldg(A.k_scale + (row0 >> P.sb_shift));
-                vs = __ldg(A.v_scale + (row0 >> P.sb_shift));
+                ks0 = __ldg(A.k_scale + (row0 >> P.sb_shift));
+                vs0 = __ldg(A.v_scale + (row0 >> P.sb_shift));
             }
-            put_scale(i0, row0, ks, vs);
         }
         // both parts of this thread's chunks of Q, while the copies fly (heads >= Hq are zeros)
 #pragma unroll
@@ -471,6 +453,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             *reinterpret_cast<uint4 *>(sm + C::kOffQ + sw<D>(c / CPH, c % CPH)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4 *>(sm + C::kOffQ + sw<D>(HQP + c / CPH, c % CPH)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
+        if (loader) put_scale(i0, row0, ks0, vs0);
         cp_async_wait_all();
         fence_async_smem();
         __syncthreads();
