@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 # SA_LIBRARY may name another build of the same library (e.g. a tuning variant)
 LIB_PATH = os.environ.get("SA_LIBRARY") or os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsa.so")
@@ -58,6 +59,7 @@ SIGNATURES = {
                                   _vp, _vp]),
     "sa_sparse_attn_q8": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _i32, _i32,
                                  _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _vp]),
+    "sa_call": (_i32, [_i32, ctypes.c_char_p, _i32]),
     "sa_pool_index_keys": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp]),
     "sa_coarse_block_counts": (_i32, [_i32, _i32, _i32, _vp, _vp]),
     "sa_expand_blocks": (_i32, [_vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp]),
@@ -203,67 +205,68 @@ def sa_sparse_attn_decode_noalloc(q, k_cache, v_cache, page_table, max_pages, po
 SA_DECODE_NOALLOC_SCRATCH_BYTES = 16 << 20
 
 
-def _on_device(where, tensors, rows=()):
-    """The one GPU that all tensors of a call are on.  tensors: (name, tensor or
-    None, dtypes, least number of elements), contiguous; rows: the same for
-    tensors of rows with a stride of their own (name, tensor, dtypes, rows, row
-    length, stride)."""
-    dev = -1
+# The entry points of the caches, below, sit between a step's small kernels,
+# so what a call costs on the host counts: their checks are one expression, and
+# the arguments go over as one array of words (sa_call) instead of one by one.
+_T = None                       # torch's types, looked up at the first call that needs them
+_CACHE_APPEND, _CACHE_APPEND_Q8, _SPARSE_ATTN_Q8 = 0, 1, 2
+_APPEND_WORDS, _APPEND_Q8_WORDS = struct.Struct("29q"), struct.Struct("32q")
+_ATTN_Q8_WORDS = struct.Struct("19qd4q")
+
+
+class _Types:
+    def __init__(self):
+        import torch
+        self.bf, self.i32, self.f32 = torch.bfloat16, torch.int32, torch.float32
+        self.f8 = (torch.uint8, torch.float8_e4m3fn)
+        self.device, self.current_device = torch.cuda.device, torch.cuda.current_device
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.raw_stream = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _types():
+    global _T
+    if _T is None:
+        _T = _Types()
+    return _T
+
+
+def _refuse(dev, tensors):
+    """Raise for the first of (name, tensor, dtypes, least number of elements) that is not a contiguous tensor of one of
+    the types on GPU `dev`: a host tensor, or a short one, never reaches a kernel."""
     for name, t, dtypes, numel in tensors:
+        dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
         if t is None:
             continue
-        at = t.get_device()
-        if at < 0 or (dev >= 0 and at != dev):
-            raise ValueError("%s: %s is not on the GPU of the other tensors" % (where, name))
-        dev = at
-        if t.dtype not in dtypes or not t.is_contiguous() or t.numel() < numel:
-            raise ValueError("%s: %s must be a contiguous %s tensor of at least %d elements"
-                             % (where, name, " or ".join(map(str, dtypes)), numel))
-    for name, t, dtypes, n, width, ld in rows:
-        if t is None:
-            continue
-        if t.get_device() != dev:
-            raise ValueError("%s: %s is not on the GPU of the other tensors" % (where, name))
-        if t.dtype not in dtypes:
-            raise ValueError("%s: %s must be a %s tensor" % (where, name, " or ".join(map(str, dtypes))))
-        if t.is_contiguous():
-            short = t.numel() < (n - 1) * ld + width
-        else:   # a slice of wider rows: [rows, width or more], ld apart
-            short = (t.dim() != 2 or t.shape[0] < n or t.shape[1] < width or t.stride(1) != 1 or t.stride(0) != ld)
-        if n > 0 and short:
-            raise ValueError("%s: %s does not hold %d rows of %d elements, %d apart" % (where, name, n, width, ld))
-    return dev
+        if dev < 0 or t.get_device() != dev:
+            raise ValueError("%s is not on the GPU of the other tensors" % name)
+        if t.dtype not in dtypes or t.numel() < numel or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous %s tensor of at least %d elements"
+                             % (name, " or ".join(map(str, dtypes)), numel))
 
 
-def _call(where, dev, stream, *args):
-    """The C call `where` on the tensors' GPU, on `stream` or that GPU's current stream."""
-    import torch
-    raw = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
-    fn = getattr(_lib, where)
-    if dev == torch.cuda.current_device():
-        status = fn(*args, raw)
+def _rows_at(t, name, dev, bf, n, width, ld):
+    """The address of n rows of `width` bf16 values, `ld` apart: contiguous, or a slice [n, width] of wider rows."""
+    if t is None:
+        return 0
+    if t.get_device() != dev or dev < 0:
+        raise ValueError("%s is not on the GPU of the other tensors" % name)
+    if t.dtype is not bf or n > 0 and (
+            t.numel() < (n - 1) * ld + width if t.is_contiguous() else
+            t.dim() != 2 or t.shape[0] < n or t.shape[1] < width or t.stride(1) != 1 or t.stride(0) != ld):
+        raise ValueError("%s does not hold %d rows of %d bf16 values, %d apart" % (name, n, width, ld))
+    return t.data_ptr()
+
+
+def _call(where, entry, dev, words):
+    """The C call on the tensors' GPU."""
+    if dev == _T.current_device():
+        status = _lib.sa_call(entry, words, len(words) // 8)
     else:
-        with torch.cuda.device(dev):
-            status = fn(*args, raw)
-    _check(status, where)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _append_args(where, q, ld_q, q_out, k, ld_k, v, ld_v, kI, ld_kI, n_valid, page_table, max_pages, pool_pages, S_max, B,
-                 T, Hq, d, D_I, inv_freq, rot_dim, k_cache, v_cache, kI_cache, kI_e4m3, dev_status, cache_dtypes, more=()):
-    import torch
-    bf, i32 = (torch.bfloat16,), (torch.int32,)
-    R, n = B * T, pool_pages * 64 if page_table is not None else B * S_max
-    byte = (torch.uint8, torch.float8_e4m3fn)
-    return _on_device(where, (
-        ("k_cache", k_cache, cache_dtypes, n * d), ("v_cache", v_cache, cache_dtypes, n * d),
-        ("n_valid", n_valid, i32, R), ("page_table", page_table, i32, B * max_pages),
-        ("q_out", q_out, bf, R * Hq * d), ("inv_freq", inv_freq, (torch.float32,), rot_dim // 2),
-        ("kI_cache", kI_cache, byte if kI_e4m3 else bf, n * D_I), ("dev_status", dev_status, i32, 1)) + more,
-        (("q", q, bf, R, Hq * d, ld_q), ("k", k, bf, R, d, ld_k), ("v", v, bf, R, d, ld_v), ("kI", kI, bf, R, D_I, ld_kI)))
+        with _T.device(dev):
+            status = _lib.sa_call(entry, words, len(words) // 8)
+    if status != SA_OK:
+        raise SAError(status, where)
 
 
 def sa_cache_append(q, ld_q, q_out, k, ld_k, v, ld_v, kI, ld_kI, n_valid, page_table, max_pages, pool_pages, page_size,
@@ -272,46 +275,103 @@ def sa_cache_append(q, ld_q, q_out, k, ld_k, v, ld_v, kI, ld_kI, n_valid, page_t
     """Append the rotated keys and the values of new tokens to a bf16 cache (and
     the index keys to theirs), and rotate the queries.  q, k, v and kI may be
     slices of wider rows (ld_* elements apart)."""
-    import torch
-    dev = _append_args("sa_cache_append", q, ld_q, q_out, k, ld_k, v, ld_v, kI, ld_kI, n_valid, page_table, max_pages,
-                       pool_pages, S_max, B, T, Hq, d, D_I, inv_freq, rot_dim, k_cache, v_cache, kI_cache, kI_e4m3,
-                       dev_status, (torch.bfloat16,))
-    _call("sa_cache_append", dev, stream, _addr(q), ld_q, _addr(q_out), _addr(k), ld_k, _addr(v), ld_v, _addr(kI), ld_kI,
-          _addr(n_valid), _addr(page_table), max_pages, pool_pages, page_size, S_max, B, T, Hq, d, D_I, _addr(inv_freq),
-          rot_dim, interleaved, _addr(k_cache), _addr(v_cache), _addr(kI_cache), kI_e4m3, _addr(dev_status))
+    t = _types()
+    bf, i32, R, n, dev = t.bf, t.i32, B * T, pool_pages * 64 if page_table is not None else B * S_max, k_cache.get_device()
+    if not (dev >= 0 and k_cache.dtype is bf and k_cache.numel() >= n * d and k_cache.is_contiguous()
+            and v_cache.get_device() == dev and v_cache.dtype is bf and v_cache.numel() >= n * d and v_cache.is_contiguous()
+            and _cache_tensors_ok(t, dev, R, n, q_out, Hq * d, n_valid, page_table, B * max_pages, inv_freq, rot_dim,
+                                  kI_cache, kI_e4m3, D_I, dev_status)):
+        _refuse(dev, (("k_cache", k_cache, bf, n * d), ("v_cache", v_cache, bf, n * d))
+                + _append_tensors(t, R, n, q_out, Hq * d, n_valid, page_table, B * max_pages, inv_freq, rot_dim, kI_cache,
+                                  kI_e4m3, D_I, dev_status))
+    _call("sa_cache_append", _CACHE_APPEND, dev, _APPEND_WORDS.pack(
+        _rows_at(q, "q", dev, bf, R, Hq * d, ld_q), ld_q, _addr(q_out), _rows_at(k, "k", dev, bf, R, d, ld_k), ld_k,
+        _rows_at(v, "v", dev, bf, R, d, ld_v), ld_v, _rows_at(kI, "kI", dev, bf, R, D_I, ld_kI), ld_kI, n_valid.data_ptr(),
+        _addr(page_table), max_pages, pool_pages, page_size, S_max, B, T, Hq, d, D_I, _addr(inv_freq), rot_dim, interleaved,
+        k_cache.data_ptr(), v_cache.data_ptr(), _addr(kI_cache), kI_e4m3, _addr(dev_status),
+        t.raw_stream(dev) if stream is None else stream.cuda_stream))
 
 
 def sa_cache_append_q8(q, ld_q, q_out, k, ld_k, v, ld_v, kI, ld_kI, n_valid, page_table, max_pages, pool_pages, page_size,
                        S_max, B, T, Hq, d, D_I, inv_freq, rot_dim, interleaved, k_cache, v_cache, k_scale, v_scale,
                        scale_block, kI_cache, kI_e4m3, dev_status=None, stream=None):
     """The same append into an 8-bit cache (uint8 or float8_e4m3fn tensors) with a scale for each scale_block tokens."""
-    import torch
-    n = (pool_pages * 64 if page_table is not None else B * S_max) // max(scale_block, 1)
-    f32, f8 = (torch.float32,), (torch.uint8, torch.float8_e4m3fn)
-    dev = _append_args("sa_cache_append_q8", q, ld_q, q_out, k, ld_k, v, ld_v, kI, ld_kI, n_valid, page_table, max_pages,
-                       pool_pages, S_max, B, T, Hq, d, D_I, inv_freq, rot_dim, k_cache, v_cache, kI_cache, kI_e4m3,
-                       dev_status, f8, (("k_scale", k_scale, f32, n), ("v_scale", v_scale, f32, n)))
-    _call("sa_cache_append_q8", dev, stream, _addr(q), ld_q, _addr(q_out), _addr(k), ld_k, _addr(v), ld_v, _addr(kI),
-          ld_kI, _addr(n_valid), _addr(page_table), max_pages, pool_pages, page_size, S_max, B, T, Hq, d, D_I,
-          _addr(inv_freq), rot_dim, interleaved, _addr(k_cache), _addr(v_cache), _addr(k_scale), _addr(v_scale),
-          scale_block, _addr(kI_cache), kI_e4m3, _addr(dev_status))
+    t = _types()
+    bf, f8, f32, R, n, dev = t.bf, t.f8, t.f32, B * T, pool_pages * 64 if page_table is not None else B * S_max, k_cache.get_device()
+    ns = n // max(scale_block, 1)
+    if not (dev >= 0 and k_cache.dtype in f8 and k_cache.numel() >= n * d and k_cache.is_contiguous()
+            and v_cache.get_device() == dev and v_cache.dtype in f8 and v_cache.numel() >= n * d and v_cache.is_contiguous()
+            and k_scale.get_device() == dev and k_scale.dtype is f32 and k_scale.numel() >= ns and k_scale.is_contiguous()
+            and v_scale.get_device() == dev and v_scale.dtype is f32 and v_scale.numel() >= ns and v_scale.is_contiguous()
+            and _cache_tensors_ok(t, dev, R, n, q_out, Hq * d, n_valid, page_table, B * max_pages, inv_freq, rot_dim,
+                                  kI_cache, kI_e4m3, D_I, dev_status)):
+        _refuse(dev, (("k_cache", k_cache, f8, n * d), ("v_cache", v_cache, f8, n * d), ("k_scale", k_scale, f32, ns),
+                      ("v_scale", v_scale, f32, ns))
+                + _append_tensors(t, R, n, q_out, Hq * d, n_valid, page_table, B * max_pages, inv_freq, rot_dim, kI_cache,
+                                  kI_e4m3, D_I, dev_status))
+    _call("sa_cache_append_q8", _CACHE_APPEND_Q8, dev, _APPEND_Q8_WORDS.pack(
+        _rows_at(q, "q", dev, bf, R, Hq * d, ld_q), ld_q, _addr(q_out), _rows_at(k, "k", dev, bf, R, d, ld_k), ld_k,
+        _rows_at(v, "v", dev, bf, R, d, ld_v), ld_v, _rows_at(kI, "kI", dev, bf, R, D_I, ld_kI), ld_kI, n_valid.data_ptr(),
+        _addr(page_table), max_pages, pool_pages, page_size, S_max, B, T, Hq, d, D_I, _addr(inv_freq), rot_dim, interleaved,
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), scale_block, _addr(kI_cache), kI_e4m3,
+        _addr(dev_status), t.raw_stream(dev) if stream is None else stream.cuda_stream))
+
+
+def _addr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _append_tensors(t, R, n, q_out, q_width, n_valid, page_table, pages, inv_freq, rot_dim, kI_cache, kI_e4m3, D_I, dev_status):
+    return (("q_out", q_out, t.bf, R * q_width), ("n_valid", n_valid, t.i32, R), ("page_table", page_table, t.i32, pages),
+            ("inv_freq", inv_freq, t.f32, rot_dim // 2), ("kI_cache", kI_cache, t.f8 if kI_e4m3 else t.bf, n * D_I),
+            ("dev_status", dev_status, t.i32, 1))
+
+
+def _cache_tensors_ok(t, dev, R, n, q_out, q_width, n_valid, page_table, pages, inv_freq, rot_dim, kI_cache, kI_e4m3, D_I,
+                      dev_status):
+    """Whether _append_tensors hold, at once."""
+    i32 = t.i32
+    return (n_valid.get_device() == dev and n_valid.dtype is i32 and n_valid.numel() >= R and n_valid.is_contiguous()
+            and (q_out is None or q_out.get_device() == dev and q_out.dtype is t.bf and q_out.numel() >= R * q_width
+                 and q_out.is_contiguous())
+            and (page_table is None or page_table.get_device() == dev and page_table.dtype is i32
+                 and page_table.numel() >= pages and page_table.is_contiguous())
+            and (inv_freq is None or inv_freq.get_device() == dev and inv_freq.dtype is t.f32
+                 and inv_freq.numel() >= rot_dim // 2 and inv_freq.is_contiguous())
+            and (kI_cache is None or kI_cache.get_device() == dev and kI_cache.numel() >= n * D_I and kI_cache.is_contiguous()
+                 and (kI_cache.dtype in t.f8 if kI_e4m3 else kI_cache.dtype is t.bf))
+            and (dev_status is None or dev_status.get_device() == dev and dev_status.dtype is i32
+                 and dev_status.numel() >= 1))
 
 
 def sa_sparse_attn_q8(q, k_cache, v_cache, k_scale, v_scale, scale_block, page_table, max_pages, pool_pages, page_size,
                       S_max, n_valid, topk, K, W, B, T, Hq, d, scale, out, lse=None, dev_status=None, stream=None):
     """Selected-key attention over an 8-bit cache, T rows a sequence."""
-    import torch
-    R, n = B * T, pool_pages * 64 if page_table is not None else B * S_max
-    i32, f32, bf = (torch.int32,), (torch.float32,), (torch.bfloat16,)
-    f8, ns = (torch.uint8, torch.float8_e4m3fn), n // max(scale_block, 1)
-    dev = _on_device("sa_sparse_attn_q8", (
-        ("q", q, bf, R * Hq * d), ("k_cache", k_cache, f8, n * d), ("v_cache", v_cache, f8, n * d),
-        ("k_scale", k_scale, f32, ns), ("v_scale", v_scale, f32, ns), ("page_table", page_table, i32, B * max_pages),
-        ("n_valid", n_valid, i32, R), ("topk", topk, i32, R * K), ("out", out, bf, R * Hq * d), ("lse", lse, f32, R * Hq),
-        ("dev_status", dev_status, i32, 1)))
-    _call("sa_sparse_attn_q8", dev, stream, _addr(q), _addr(k_cache), _addr(v_cache), _addr(k_scale), _addr(v_scale),
-          scale_block, _addr(page_table), max_pages, pool_pages, page_size, S_max, _addr(n_valid), _addr(topk), K, W, B, T,
-          Hq, d, scale, _addr(out), _addr(lse), _addr(dev_status))
+    t = _types()
+    R, n, dev = B * T, pool_pages * 64 if page_table is not None else B * S_max, q.get_device()
+    bf, f8, f32, i32, ns = t.bf, t.f8, t.f32, t.i32, n // max(scale_block, 1)
+    if not (dev >= 0 and q.dtype is bf and q.numel() >= R * Hq * d and q.is_contiguous()
+            and k_cache.get_device() == dev and k_cache.dtype in f8 and k_cache.numel() >= n * d and k_cache.is_contiguous()
+            and v_cache.get_device() == dev and v_cache.dtype in f8 and v_cache.numel() >= n * d and v_cache.is_contiguous()
+            and k_scale.get_device() == dev and k_scale.dtype is f32 and k_scale.numel() >= ns and k_scale.is_contiguous()
+            and v_scale.get_device() == dev and v_scale.dtype is f32 and v_scale.numel() >= ns and v_scale.is_contiguous()
+            and n_valid.get_device() == dev and n_valid.dtype is i32 and n_valid.numel() >= R and n_valid.is_contiguous()
+            and out.get_device() == dev and out.dtype is bf and out.numel() >= R * Hq * d and out.is_contiguous()
+            and (topk is None or topk.get_device() == dev and topk.dtype is i32 and topk.numel() >= R * K
+                 and topk.is_contiguous())
+            and (page_table is None or page_table.get_device() == dev and page_table.dtype is i32
+                 and page_table.numel() >= B * max_pages and page_table.is_contiguous())
+            and (lse is None or lse.get_device() == dev and lse.dtype is f32 and lse.numel() >= R * Hq and lse.is_contiguous())
+            and (dev_status is None or dev_status.get_device() == dev and dev_status.dtype is i32
+                 and dev_status.numel() >= 1)):
+        _refuse(dev, (("q", q, bf, R * Hq * d), ("k_cache", k_cache, f8, n * d), ("v_cache", v_cache, f8, n * d),
+                      ("k_scale", k_scale, f32, ns), ("v_scale", v_scale, f32, ns), ("n_valid", n_valid, i32, R),
+                      ("out", out, bf, R * Hq * d), ("topk", topk, i32, R * K), ("page_table", page_table, i32, B * max_pages),
+                      ("lse", lse, f32, R * Hq), ("dev_status", dev_status, i32, 1)))
+    _call("sa_sparse_attn_q8", _SPARSE_ATTN_Q8, dev, _ATTN_Q8_WORDS.pack(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), scale_block,
+        _addr(page_table), max_pages, pool_pages, page_size, S_max, n_valid.data_ptr(), _addr(topk), K, W, B, T, Hq, d, scale,
+        out.data_ptr(), _addr(lse), _addr(dev_status), t.raw_stream(dev) if stream is None else stream.cuda_stream))
 
 
 def sa_pool_index_keys(kI, S, D_I, block, kB, stream=None):

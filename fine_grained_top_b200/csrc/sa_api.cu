@@ -2,6 +2,10 @@
 // then kernel launches on the caller's stream.  Nothing is enqueued when a
 // check fails; no C++ exception crosses the boundary; nothing is allocated.
 #include <stdint.h>
+#include <string.h>
+
+#include <tuple>
+#include <type_traits>
 
 #include "../../include/sa.h"
 #include "internal.h"
@@ -24,6 +28,43 @@ sa_status guarded(F &&f) {
     } catch (...) {
         return SA_ERR_CUDA;
     }
+}
+
+// Unpacks an array of words into the call's own argument types (an integer that
+// does not fit is an error, not a truncation).
+struct Words {
+    const unsigned char *at;
+    bool ok = true;
+    int64_t word() {
+        int64_t v;
+        memcpy(&v, at, 8);
+        at += 8;
+        return v;
+    }
+    template <class T>
+    void take(T &v) {
+        if constexpr (std::is_pointer_v<T>) {
+            v = reinterpret_cast<T>(static_cast<uintptr_t>(word()));
+        } else if constexpr (std::is_floating_point_v<T>) {
+            double d;
+            memcpy(&d, at, 8);
+            at += 8;
+            v = static_cast<T>(d);
+        } else {
+            const int64_t w = word();
+            v = static_cast<T>(w);
+            ok = ok && static_cast<int64_t>(v) == w;
+        }
+    }
+};
+
+template <class... A>
+sa_status call_words(sa_status (*fn)(A...), const void *words, int n_words) {
+    if (n_words != (int)sizeof...(A)) return SA_ERR_INVALID_ARG;
+    Words w{static_cast<const unsigned char *>(words)};
+    std::tuple<A...> args;
+    std::apply([&](auto &...a) { (w.take(a), ...); }, args);
+    return w.ok ? std::apply(fn, args) : SA_ERR_INVALID_ARG;
 }
 
 }  // namespace
@@ -330,6 +371,16 @@ sa_status sa_sparse_attn_q8(const sa_bf16 *q, const sa_e4m3 *k_cache, const sa_e
         a.T = T; a.Hq = Hq; a.d = d; a.scale = scale; a.out = out; a.lse = lse; a.dev_status = dev_status;
         return launch_attn_q8(a, cs(stream));
     });
+}
+
+sa_status sa_call(sa_call_entry entry, const void *words, int n_words) {
+    if (!words) return SA_ERR_INVALID_ARG;
+    switch (entry) {
+        case SA_CALL_CACHE_APPEND: return call_words(sa_cache_append, words, n_words);
+        case SA_CALL_CACHE_APPEND_Q8: return call_words(sa_cache_append_q8, words, n_words);
+        case SA_CALL_SPARSE_ATTN_Q8: return call_words(sa_sparse_attn_q8, words, n_words);
+    }
+    return SA_ERR_INVALID_ARG;
 }
 
 sa_status sa_pool_index_keys(const sa_bf16 *kI, int S, int D_I, int block, sa_bf16 *kB, sa_stream stream) {

@@ -509,6 +509,20 @@ sa_status sa_sparse_attn_q8(const sa_bf16 *q, const sa_e4m3 *k_cache,
                             sa_bf16 *out, float *lse, int *dev_status,
                             sa_stream stream);
 
+/* The three calls above with their arguments as one array of 64-bit words, in
+ * order: pointers and integers as they are, a float as a double (for bindings
+ * whose cost goes by the argument: a step makes these calls between kernels
+ * of a few microseconds).  n_words must be the entry's number of arguments and
+ * every integer must fit its parameter: SA_ERR_INVALID_ARG otherwise.  words
+ * is host memory, any alignment. */
+typedef enum {
+    SA_CALL_CACHE_APPEND = 0,      /* sa_cache_append, 29 words    */
+    SA_CALL_CACHE_APPEND_Q8 = 1,   /* sa_cache_append_q8, 32 words */
+    SA_CALL_SPARSE_ATTN_Q8 = 2     /* sa_sparse_attn_q8, 24 words  */
+} sa_call_entry;
+
+sa_status sa_call(sa_call_entry entry, const void *words, int n_words);
+
 /* ------------------------------------------------------------------------
  * Two-stage selection helpers ("What Fine-Grained Means": a coarse block pass
  * picks candidate regions cheaply, a fine pass picks top-K tokens inside

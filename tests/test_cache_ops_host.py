@@ -2,6 +2,7 @@
 attention (no GPU: the checks run before any CUDA call)."""
 
 import ctypes
+import struct
 
 import pytest
 import torch
@@ -85,6 +86,26 @@ def attn_args(**kw):
 def test_attention_q8_refusals(sa, kw, want):
     code = sa.SA_OK if want == "OK" else getattr(sa, "SA_ERR_" + want)
     assert sa._lib.sa_sparse_attn_q8(*attn_args(**kw)) == code
+
+
+def test_calls_by_words(sa):
+    """sa_call checks its words and hands them to the same checks as the call itself."""
+    f, S = sa._lib.sa_call, struct.Struct("19qd4q")
+    a = [0 if v is None else getattr(v, "value", v) for v in attn_args()]
+    assert f(2, S.pack(*attn_words(B=0)), 24) == sa.SA_OK
+    assert f(2, S.pack(*attn_words(d=32)), 24) == sa.SA_ERR_UNSUPPORTED
+    assert f(2, S.pack(*a), 23) == sa.SA_ERR_INVALID_ARG                      # a word short
+    assert f(3, S.pack(*a), 24) == sa.SA_ERR_INVALID_ARG                      # no such entry
+    assert f(2, None, 24) == sa.SA_ERR_INVALID_ARG
+    assert f(2, S.pack(*attn_words(B=2 ** 32)), 24) == sa.SA_ERR_INVALID_ARG   # would be 0 in 32 bits
+    w = [0 if v is None else getattr(v, "value", v) for v in append_args(T=0)]
+    assert f(0, struct.pack("29q", *w), 29) == sa.SA_OK
+    w = [0 if v is None else getattr(v, "value", v) for v in append_args(q8=True, rot_dim=8)]
+    assert f(1, struct.pack("32q", *w), 32) == sa.SA_ERR_UNSUPPORTED
+
+
+def attn_words(**kw):
+    return [0 if v is None else getattr(v, "value", v) for v in attn_args(**kw)]
 
 
 def test_tensors_of_the_wrong_kind_are_refused(sa):
