@@ -119,11 +119,46 @@ __device__ __forceinline__ void rotate8(uint4 &a, uint4 &b, const float2 *cs) {
 }
 
 template <bool INTER>
-__device__ void append_rows(const AppendParams &P, int cta, float2 (*cs)[64], int64_t *slot, int *pos) {
+__device__ __forceinline__ void append_rows(const AppendParams &P, int cta, float2 (*cs)[64], int64_t *slot, int *pos) {
     const AppendArgs &a = P.a;
-    const int R = a.B * a.T, r0 = cta * P.rows, nr = min(P.rows, R - r0), half = a.rot_dim / 2;
-    if (threadIdx.x < nr) {
-        const int r = r0 + threadIdx.x, n = a.n_valid[r];
+    const int R = a.B * a.T, r0 = cta * P.rows, nr = min(P.rows, R - r0), half = a.rot_dim / 2, tid = threadIdx.x;
+    const int u_heads = P.heads * P.u_head, n_units = nr * P.u_row;
+    // unit i: a chunk of 8 values (x), or the two halves of a pair of chunks (x, y)
+    struct Unit {
+        int rl, h, c;   // row; head, or P.heads: value and index key; chunk
+    };
+    auto unit = [&](int i) {
+        Unit t;
+        t.rl = (int)(((uint64_t)i * P.m_row) >> 24);
+        const int u = i - t.rl * P.u_row;
+        t.h = u < u_heads ? (int)((u * P.m_head) >> 16) : P.heads;
+        t.c = u - t.h * P.u_head;
+        return t;
+    };
+    auto load = [&](const Unit &t, uint4 &x, uint4 &y) {
+        const int64_t r = r0 + t.rl;
+        y = make_uint4(0, 0, 0, 0);
+        if (t.h < P.heads) {
+            const uint16_t *src = t.h == a.Hq ? a.k + r * a.ld_k : a.q + r * a.ld_q + t.h * a.d;
+            const bool rot = t.c < P.u_rot;
+            x = *reinterpret_cast<const uint4 *>(src + (rot ? t.c * 8 : a.rot_dim + (t.c - P.u_rot) * 8));
+            if (!INTER && rot) y = *reinterpret_cast<const uint4 *>(src + half + t.c * 8);
+        } else {
+            const int c = t.c * 8;
+            x = c < a.d ? *reinterpret_cast<const uint4 *>(a.v + r * a.ld_v + c)
+                        : *reinterpret_cast<const uint4 *>(a.kI + r * a.ld_kI + (c - a.d));
+        }
+    };
+    // the first turn's values are on their way while the angles are computed
+    Unit t = {};
+    uint4 x = {}, y = {};
+    if (tid < n_units) load(t = unit(tid), x, y);
+    for (int i = tid; i < nr * half; i += kAThreads) {
+        const int rl = i / half, f = i - rl * half, n = __ldg(a.n_valid + r0 + rl);
+        if (n > 0) cs[rl][f] = turn(n - 1, __ldg(a.inv_freq + f));
+    }
+    if (tid >= kAThreads - 32 && tid - (kAThreads - 32) < nr) {   // (the angles rarely reach the last warp)
+        const int rl = tid - (kAThreads - 32), r = r0 + rl, n = __ldg(a.n_valid + r);
         int p = n - 1;
         int64_t s = -1;
         if (n < 0 || n > a.S_max) {
@@ -133,50 +168,35 @@ __device__ void append_rows(const AppendParams &P, int cta, float2 (*cs)[64], in
             s = cache_slot(a, r / a.T, p);
             if (s < 0) report(a.dev_status, SA_DEV_INDEX);
         }
-        pos[threadIdx.x] = p;
-        slot[threadIdx.x] = s;
+        pos[rl] = p;
+        slot[rl] = s;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < nr * half; i += kAThreads) {
-        const int rl = i / half, f = i - rl * half;
-        if (pos[rl] >= 0) cs[rl][f] = turn(pos[rl], __ldg(a.inv_freq + f));
-    }
-    __syncthreads();
-    const int u_heads = P.heads * P.u_head;
-    for (int i = threadIdx.x; i < nr * P.u_row; i += kAThreads) {
-        const int rl = (int)(((uint64_t)i * P.m_row) >> 24), u = i - rl * P.u_row;
-        if (pos[rl] < 0) continue;
-        const int64_t r = r0 + rl;
-        if (u < u_heads) {
-            const int h = (int)((u * P.m_head) >> 16), c = u - h * P.u_head;
-            const bool is_k = h == a.Hq;   // the row's key (16-bit cache)
-            if (is_k && slot[rl] < 0) continue;
-            const uint16_t *src = is_k ? a.k + r * a.ld_k : a.q + r * a.ld_q + h * a.d;
-            uint16_t *dst = is_k ? static_cast<uint16_t *>(a.k_cache) + slot[rl] * a.d : a.q_out + (r * a.Hq + h) * a.d;
-            if (c < P.u_rot) {
-                uint4 x = *reinterpret_cast<const uint4 *>(src + c * 8), y = make_uint4(0, 0, 0, 0);
-                if (!INTER) y = *reinterpret_cast<const uint4 *>(src + half + c * 8);
-                rotate8<INTER>(x, y, &cs[rl][INTER ? 4 * c : 8 * c]);
-                *reinterpret_cast<uint4 *>(dst + c * 8) = x;
-                if (!INTER) *reinterpret_cast<uint4 *>(dst + half + c * 8) = y;
+    for (int i = tid; i < n_units;) {
+        const bool is_k = t.h == a.Hq && t.h < P.heads;   // the row's key (16-bit cache)
+        const int64_t r = r0 + t.rl, sl = slot[t.rl];
+        if (pos[t.rl] < 0 || (t.h >= a.Hq && sl < 0)) {
+            // padding, or no slot to write
+        } else if (t.h < P.heads) {
+            uint16_t *dst = is_k ? static_cast<uint16_t *>(a.k_cache) + sl * a.d : a.q_out + (r * a.Hq + t.h) * a.d;
+            if (t.c < P.u_rot) {
+                rotate8<INTER>(x, y, &cs[t.rl][INTER ? 4 * t.c : 8 * t.c]);
+                *reinterpret_cast<uint4 *>(dst + t.c * 8) = x;
+                if (!INTER) *reinterpret_cast<uint4 *>(dst + half + t.c * 8) = y;
             } else {
-                const int o = a.rot_dim + (c - P.u_rot) * 8;
-                *reinterpret_cast<uint4 *>(dst + o) = *reinterpret_cast<const uint4 *>(src + o);
+                *reinterpret_cast<uint4 *>(dst + a.rot_dim + (t.c - P.u_rot) * 8) = x;
             }
-        } else if (slot[rl] >= 0) {
-            const int c = (u - u_heads) * 8;
-            if (c < a.d) {
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.v_cache) + slot[rl] * a.d + c) =
-                    *reinterpret_cast<const uint4 *>(a.v + r * a.ld_v + c);
-            } else {
-                const uint4 x = *reinterpret_cast<const uint4 *>(a.kI + r * a.ld_kI + (c - a.d));
-                const int64_t o = slot[rl] * a.D_I + (c - a.d);
-                if (a.kI_e4m3)
-                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.kI_cache) + o) = e4m3_of8(x);
-                else
-                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.kI_cache) + o) = x;
-            }
+        } else {
+            const int c = t.c * 8;
+            if (c < a.d)
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.v_cache) + sl * a.d + c) = x;
+            else if (a.kI_e4m3)
+                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.kI_cache) + sl * a.D_I + (c - a.d)) = e4m3_of8(x);
+            else
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.kI_cache) + sl * a.D_I + (c - a.d)) = x;
         }
+        i += kAThreads;
+        if (i < n_units) load(t = unit(i), x, y);
     }
 }
 
@@ -254,25 +274,24 @@ __device__ void append_page(const AppendParams &P, int job, uint32_t (*amax)[kAP
     const bool rot = d0 < a.rot_dim;
     const int partner = INTER ? lane : (lane < hl ? lane + hl : (lane < 2 * hl ? lane - hl : lane));
     const bool upper = !INTER && lane >= hl;
-    float kx[NT][NV], vx[NT][NV];
+    float kx[NT][NV];
+    uint32_t vw[NT][NV / 2];   // values as they came, in bf16
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         const int tok = i * NW + warp;
         if (tok >= m) break;   // the same for the whole warp
         const uint16_t *kr = a.k + (row0 + tok) * a.ld_k + d0, *vr = a.v + (row0 + tok) * a.ld_v + d0;
-        uint32_t kw[NV / 2], vw[NV / 2];
+        uint32_t kw[NV / 2];
 #pragma unroll
         for (int e = 0; e < NV / 2; ++e) {
             kw[e] = __ldg(reinterpret_cast<const uint32_t *>(kr) + e);
-            vw[e] = __ldg(reinterpret_cast<const uint32_t *>(vr) + e);
+            vw[i][e] = __ldg(reinterpret_cast<const uint32_t *>(vr) + e);
         }
         float x[NV];
 #pragma unroll
         for (int e = 0; e < NV / 2; ++e) {
             x[2 * e] = bf_lo(kw[e]);
             x[2 * e + 1] = bf_hi(kw[e]);
-            vx[i][2 * e] = bf_lo(vw[e]);
-            vx[i][2 * e + 1] = bf_hi(vw[e]);
         }
         if (INTER) {
 #pragma unroll
@@ -304,7 +323,7 @@ __device__ void append_page(const AppendParams &P, int job, uint32_t (*amax)[kAP
 #pragma unroll
         for (int e = 0; e < NV; ++e) {
             mk = max(mk, finite_abs(kx[i][e]));
-            mv = max(mv, finite_abs(vx[i][e]));
+            mv = max(mv, finite_abs(e & 1 ? bf_hi(vw[i][e / 2]) : bf_lo(vw[i][e / 2])));
         }
         mk = __reduce_max_sync(0xffffffffu, mk);
         mv = __reduce_max_sync(0xffffffffu, mv);
@@ -353,7 +372,10 @@ __device__ void append_page(const AppendParams &P, int job, uint32_t (*amax)[kAP
         const int blk = (o0 + tok) / sb;
         const int64_t o = (base + o0 + tok) * D;
         store_codes<NV>(static_cast<uint8_t *>(a.k_cache) + o, lane, kx[i], scale[0][blk]);
-        store_codes<NV>(static_cast<uint8_t *>(a.v_cache) + o, lane, vx[i], scale[1][blk]);
+        float vx[NV];
+#pragma unroll
+        for (int e = 0; e < NV; ++e) vx[e] = e & 1 ? bf_hi(vw[i][e / 2]) : bf_lo(vw[i][e / 2]);
+        store_codes<NV>(static_cast<uint8_t *>(a.v_cache) + o, lane, vx, scale[1][blk]);
     }
     // earlier tokens of a block whose scale grew
     const int words = (o0 - blk0 * sb) * (D / 4);
@@ -371,18 +393,29 @@ __device__ void append_page(const AppendParams &P, int job, uint32_t (*amax)[kAP
     }
 }
 
-template <int D, bool INTER>
-__global__ void __launch_bounds__(kAThreads) append_kernel(AppendParams P) {
+// (The page CTAs of the 8-bit form hold a page's keys and values in registers,
+// 64 a thread; rows alone need half of that.)
+template <int D, bool INTER, bool Q8>
+__global__ void __launch_bounds__(kAThreads, Q8 ? 4 : 6) append_kernel(AppendParams P) {
     __shared__ float2 cs[kARowsMax][64];
     __shared__ int64_t slot[kARowsMax];
     __shared__ int pos[kARowsMax];
-    __shared__ uint32_t amax[2][kAPage];
-    __shared__ float scale[2][kAPage], ratio[2];
-    __shared__ int red[4];
-    if ((int)blockIdx.x < P.n_page_ctas)
-        append_page<D, INTER>(P, (int)blockIdx.x, amax, scale, red, ratio);
-    else
-        append_rows<INTER>(P, (int)blockIdx.x - P.n_page_ctas, cs, slot, pos);
+    if constexpr (Q8) {
+        if ((int)blockIdx.x < P.n_page_ctas) {
+            __shared__ uint32_t amax[2][kAPage];
+            __shared__ float scale[2][kAPage], ratio[2];
+            __shared__ int red[4];
+            append_page<D, INTER>(P, (int)blockIdx.x, amax, scale, red, ratio);
+            return;
+        }
+    }
+    append_rows<INTER>(P, (int)blockIdx.x - P.n_page_ctas, cs, slot, pos);
+}
+
+template <int D, bool INTER>
+void launch_append_kernel(const AppendParams &P, unsigned grid, cudaStream_t st) {
+    if (P.a.q8) append_kernel<D, INTER, true><<<grid, kAThreads, 0, st>>>(P);
+    else append_kernel<D, INTER, false><<<grid, kAThreads, 0, st>>>(P);
 }
 
 }  // namespace
@@ -406,11 +439,11 @@ sa_status launch_append(const AppendArgs &a, cudaStream_t st) {
     const unsigned grid = (unsigned)(n_page + n_rows);
     if (grid == 0) return SA_OK;
     if (a.d == 128) {
-        if (a.interleaved) append_kernel<128, true><<<grid, kAThreads, 0, st>>>(P);
-        else append_kernel<128, false><<<grid, kAThreads, 0, st>>>(P);
+        if (a.interleaved) launch_append_kernel<128, true>(P, grid, st);
+        else launch_append_kernel<128, false>(P, grid, st);
     } else {
-        if (a.interleaved) append_kernel<64, true><<<grid, kAThreads, 0, st>>>(P);
-        else append_kernel<64, false><<<grid, kAThreads, 0, st>>>(P);
+        if (a.interleaved) launch_append_kernel<64, true>(P, grid, st);
+        else launch_append_kernel<64, false>(P, grid, st);
     }
     return cuda_ok(cudaGetLastError());
 }

@@ -401,7 +401,7 @@ sa_status sa_sparse_attn_decode_noalloc(const sa_bf16 *q,
  *   is token t of sequence b; n_valid[r] is its position + 1 (the number of
  *   cached tokens it sees once the step is appended, as sa_indexer_scores and
  *   sa_sparse_attn_q8 take it), or 0 for a padding row, of which nothing is
- *   read and nothing written.  With p = n_valid[r] - 1:
+ *   written.  With p = n_valid[r] - 1:
  *     a_i = p * inv_freq[i], i < rot_dim / 2, and the pairs (i, i + rot_dim/2)
  *     or, with interleaved != 0, (2i, 2i + 1) of every head turn by it:
  *       x'_first = x_first cos a_i - x_second sin a_i
