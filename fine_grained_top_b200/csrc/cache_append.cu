@@ -149,10 +149,15 @@ __device__ __forceinline__ void append_rows(const AppendParams &P, int cta, floa
                         : *reinterpret_cast<const uint4 *>(a.kI + r * a.ld_kI + (c - a.d));
         }
     };
-    // the first turn's values are on their way while the angles are computed
-    Unit t = {};
-    uint4 x = {}, y = {};
-    if (tid < n_units) load(t = unit(tid), x, y);
+    // two units a turn; the first turn's values are on their way while the angles are computed
+    Unit t[2] = {};
+    uint4 x[2] = {}, y[2] = {};
+    auto load2 = [&](int i) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (i + k * kAThreads < n_units) load(t[k] = unit(i + k * kAThreads), x[k], y[k]);
+    };
+    load2(tid);
     for (int i = tid; i < nr * half; i += kAThreads) {
         const int rl = i / half, f = i - rl * half, n = __ldg(a.n_valid + r0 + rl);
         if (n > 0) cs[rl][f] = turn(n - 1, __ldg(a.inv_freq + f));
@@ -173,30 +178,33 @@ __device__ __forceinline__ void append_rows(const AppendParams &P, int cta, floa
     }
     __syncthreads();
     for (int i = tid; i < n_units;) {
-        const bool is_k = t.h == a.Hq && t.h < P.heads;   // the row's key (16-bit cache)
-        const int64_t r = r0 + t.rl, sl = slot[t.rl];
-        if (pos[t.rl] < 0 || (t.h >= a.Hq && sl < 0)) {
-            // padding, or no slot to write
-        } else if (t.h < P.heads) {
-            uint16_t *dst = is_k ? static_cast<uint16_t *>(a.k_cache) + sl * a.d : a.q_out + (r * a.Hq + t.h) * a.d;
-            if (t.c < P.u_rot) {
-                rotate8<INTER>(x, y, &cs[t.rl][INTER ? 4 * t.c : 8 * t.c]);
-                *reinterpret_cast<uint4 *>(dst + t.c * 8) = x;
-                if (!INTER) *reinterpret_cast<uint4 *>(dst + half + t.c * 8) = y;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const Unit &w = t[k];
+            const bool is_k = w.h == a.Hq && w.h < P.heads;   // the row's key (16-bit cache)
+            const int64_t r = r0 + w.rl, sl = slot[w.rl];
+            if (i + k * kAThreads >= n_units || pos[w.rl] < 0 || (w.h >= a.Hq && sl < 0)) continue;   // (padding, no slot)
+            if (w.h < P.heads) {
+                uint16_t *dst = is_k ? static_cast<uint16_t *>(a.k_cache) + sl * a.d : a.q_out + (r * a.Hq + w.h) * a.d;
+                if (w.c < P.u_rot) {
+                    rotate8<INTER>(x[k], y[k], &cs[w.rl][INTER ? 4 * w.c : 8 * w.c]);
+                    *reinterpret_cast<uint4 *>(dst + w.c * 8) = x[k];
+                    if (!INTER) *reinterpret_cast<uint4 *>(dst + half + w.c * 8) = y[k];
+                } else {
+                    *reinterpret_cast<uint4 *>(dst + a.rot_dim + (w.c - P.u_rot) * 8) = x[k];
+                }
             } else {
-                *reinterpret_cast<uint4 *>(dst + a.rot_dim + (t.c - P.u_rot) * 8) = x;
+                const int c = w.c * 8;
+                if (c < a.d)
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.v_cache) + sl * a.d + c) = x[k];
+                else if (a.kI_e4m3)
+                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.kI_cache) + sl * a.D_I + (c - a.d)) = e4m3_of8(x[k]);
+                else
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.kI_cache) + sl * a.D_I + (c - a.d)) = x[k];
             }
-        } else {
-            const int c = t.c * 8;
-            if (c < a.d)
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.v_cache) + sl * a.d + c) = x;
-            else if (a.kI_e4m3)
-                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.kI_cache) + sl * a.D_I + (c - a.d)) = e4m3_of8(x);
-            else
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.kI_cache) + sl * a.D_I + (c - a.d)) = x;
         }
-        i += kAThreads;
-        if (i < n_units) load(t = unit(i), x, y);
+        i += 2 * kAThreads;
+        load2(i);
     }
 }
 
