@@ -16,11 +16,11 @@
 //          chunks) per thread and turn; cosines and sines once a row in shared
 //          memory, used by all of its heads.  With a 16-bit cache the key is one
 //          more head of the row, value and index key are copied beside it.
-//   pages: (8-bit caches) the new tokens of one 64-token page, so that every
-//          scale block has one owner whatever its length: a warp holds a
-//          token's key and value in registers (d / 32 values a lane, pair
-//          partners exchanged by shuffles), block maxima meet in shared memory,
-//          and codes are made from the registers once the scales are known.
+//   pages: (8-bit caches) the new keys or values of one 64-token page, so that
+//          every scale block has one owner whatever its length: a warp holds a
+//          token in registers (d / 32 values a lane, pair partners exchanged by
+//          shuffles), block maxima meet in shared memory, and codes are made
+//          from the registers once the scales are known.
 #include <algorithm>
 
 #include "internal.h"
@@ -37,7 +37,7 @@ constexpr int kAPage = 64;
 struct AppendParams {
     AppendArgs a;
     int n_page_ctas;     // CTAs of the page kind, first in the grid (8-bit caches)
-    int jobs;            // page CTAs a sequence
+    int jobs;            // pages a sequence
     int rows;            // rows per row CTA
     int heads;           // heads a row CTA rotates: Hq, and the key with a 16-bit cache
     int u_rot, u_head;   // rotating chunks (or chunk pairs) and all units of a head
@@ -224,91 +224,111 @@ __device__ __forceinline__ uint32_t finite_abs(float x) {   // bits of |x|, 0 fo
     return b < 0x7F800000u ? b : 0u;
 }
 
-template <int D, bool INTER>
-__device__ void append_page(const AppendParams &P, int job, uint32_t (*amax)[kAPage], float (*scale)[kAPage], int *red,
-                            float *ratio) {
+// One side of a page: its new keys (rotated) or values.
+template <int D, bool INTER, bool KEYS>
+__device__ __forceinline__ void append_page(const AppendParams &P, int job, uint32_t *amax, float *scale, int *red, float *ratio) {
     constexpr int NV = D / 32, NW = kAThreads / 32, NT = kAPage / NW;   // values a lane, warps, tokens a warp
     const AppendArgs &a = P.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int b = job / P.jobs, j = job - b * P.jobs;
     const int32_t *nv = a.n_valid + (int64_t)b * a.T;
 
-    // the sequence's run of valid rows, checked: red = first, last, count, errors
-    if (tid < 4) red[tid] = tid == 0 ? a.T : (tid == 1 ? -1 : 0);
-    for (int i = tid; i < 2 * kAPage; i += kAThreads) amax[i / kAPage][i % kAPage] = 0;
-    __syncthreads();
-    int first = a.T, last = -1, count = 0, err = 0;
-    for (int t = tid; t < a.T; t += kAThreads) {
-        const int n = __ldg(nv + t);
-        if (n < 0 || n > a.S_max) err |= SA_DEV_INDEX;
-        if (n > 0) {
-            const int before = t > 0 ? __ldg(nv + t - 1) : 0;
-            if (before > 0 && n != before + 1) err |= SA_DEV_ORDER;
-            first = min(first, t);
-            last = max(last, t);
-            ++count;
+    // the sequence's run of valid rows, checked
+    if (tid < kAPage) amax[tid] = 0;
+    if (tid == 0) *ratio = 1.f;
+    int first = 0, count, err = 0, n0;   // n0: n_valid of the run's first row
+    if (a.T == 1) {
+        n0 = __ldg(nv);
+        count = n0 > 0;
+        if (n0 < 0 || n0 > a.S_max) err = SA_DEV_INDEX;
+        __syncthreads();
+    } else {   // red: first, last, count, errors
+        if (tid < 4) red[tid] = tid == 0 ? a.T : (tid == 1 ? -1 : 0);
+        __syncthreads();
+        int last = -1;
+        first = a.T;
+        count = 0;
+        for (int t = tid; t < a.T; t += kAThreads) {
+            const int n = __ldg(nv + t);
+            if (n < 0 || n > a.S_max) err |= SA_DEV_INDEX;
+            if (n > 0) {
+                const int before = t > 0 ? __ldg(nv + t - 1) : 0;
+                if (before > 0 && n != before + 1) err |= SA_DEV_ORDER;
+                first = min(first, t);
+                last = max(last, t);
+                ++count;
+            }
         }
+        if (last >= 0) {
+            atomicMin(&red[0], first);
+            atomicMax(&red[1], last);
+            atomicAdd(&red[2], count);
+        }
+        if (err) atomicOr(&red[3], err);
+        __syncthreads();
+        first = red[0];
+        count = red[2];
+        err = red[3];
+        if (count > 0 && red[1] - first + 1 != count) err |= SA_DEV_ORDER;   // a gap
+        n0 = count > 0 ? __ldg(nv + first) : 0;
     }
-    if (last >= 0) {
-        atomicMin(&red[0], first);
-        atomicMax(&red[1], last);
-        atomicAdd(&red[2], count);
-    }
-    if (err) atomicOr(&red[3], err);
-    __syncthreads();
-    first = red[0];
-    count = red[2];
-    err = red[3];
-    if (count > 0 && red[1] - first + 1 != count) err |= SA_DEV_ORDER;   // a gap
     if (err & SA_DEV_INDEX) err = SA_DEV_INDEX;   // a number out of range is no successor either: one error
     if (err || count == 0) {
         if (err && j == 0 && tid == 0) report(a.dev_status, err);
         return;
     }
-    const int p0 = __ldg(nv + first) - 1, page = p0 / kAPage + j;
+    const int p0 = n0 - 1, page = p0 / kAPage + j;
     const int begin = max(p0, page * kAPage), m = min(p0 + count, (page + 1) * kAPage) - begin;
     if (m <= 0) return;
     const int64_t base = cache_slot(a, b, page * kAPage);   // the page's first slot
-    if (base < 0) {
-        if (tid == 0) report(a.dev_status, SA_DEV_INDEX);
-        return;
-    }
     const int o0 = begin % kAPage, sb = a.scale_block;
     const int64_t row0 = (int64_t)b * a.T + first + (begin - p0);
+    const uint16_t *src = KEYS ? a.k : a.v;
+    const int64_t ld = KEYS ? a.ld_k : a.ld_v;
+    uint8_t *cache = static_cast<uint8_t *>(KEYS ? a.k_cache : a.v_cache);
 
-    // keys (rotated) and values of this warp's tokens warp, warp + NW, ...
+    // this warp's tokens warp, warp + NW, ...
     const int half = a.rot_dim / 2, hl = half / NV;      // lanes of one half of the rotated dims
     const int d0 = lane * NV;                            // this lane's first dim
     const bool rot = d0 < a.rot_dim;
     const int partner = INTER ? lane : (lane < hl ? lane + hl : (lane < 2 * hl ? lane - hl : lane));
     const bool upper = !INTER && lane >= hl;
-    float kx[NT][NV];
-    uint32_t vw[NT][NV / 2];   // values as they came, in bf16
+    uint32_t w[NT][NV / 2];   // the values as they came, in bf16
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         const int tok = i * NW + warp;
         if (tok >= m) break;   // the same for the whole warp
-        const uint16_t *kr = a.k + (row0 + tok) * a.ld_k + d0, *vr = a.v + (row0 + tok) * a.ld_v + d0;
-        uint32_t kw[NV / 2];
 #pragma unroll
-        for (int e = 0; e < NV / 2; ++e) {
-            kw[e] = __ldg(reinterpret_cast<const uint32_t *>(kr) + e);
-            vw[i][e] = __ldg(reinterpret_cast<const uint32_t *>(vr) + e);
-        }
-        float x[NV];
+        for (int e = 0; e < NV / 2; ++e)
+            w[i][e] = __ldg(reinterpret_cast<const uint32_t *>(src + (row0 + tok) * ld + d0) + e);
+    }
+    if (base < 0) {
+        if (tid == 0) report(a.dev_status, SA_DEV_INDEX);
+        return;
+    }
+    // the old scale of a block that holds earlier tokens (the first one, if any)
+    const int blk0 = o0 / sb, blk1 = (o0 + m - 1) / sb;
+    float *scales = (KEYS ? a.k_scale : a.v_scale) + base / sb;
+    const bool partial = blk0 * sb < o0;
+    const float was = partial && tid == 0 ? scales[blk0] : 0.f;
+    float x[NT][NV];
 #pragma unroll
-        for (int e = 0; e < NV / 2; ++e) {
-            x[2 * e] = bf_lo(kw[e]);
-            x[2 * e + 1] = bf_hi(kw[e]);
-        }
-        if (INTER) {
+    for (int i = 0; i < NT; ++i) {
+        const int tok = i * NW + warp;
+        if (tok >= m) break;
+        float y[NV];
+#pragma unroll
+        for (int e = 0; e < NV; ++e) x[i][e] = y[e] = e & 1 ? bf_hi(w[i][e / 2]) : bf_lo(w[i][e / 2]);
+        if (KEYS && INTER) {
 #pragma unroll
             for (int e = 0; e < NV / 2; ++e) {
                 const float2 c = rot ? turn(begin + tok, __ldg(a.inv_freq + d0 / 2 + e)) : make_float2(1.f, 0.f);
-                kx[i][2 * e] = rot ? x[2 * e] * c.x - x[2 * e + 1] * c.y : x[2 * e];
-                kx[i][2 * e + 1] = rot ? x[2 * e + 1] * c.x + x[2 * e] * c.y : x[2 * e + 1];
+                if (rot) {
+                    x[i][2 * e] = y[2 * e] * c.x - y[2 * e + 1] * c.y;
+                    x[i][2 * e + 1] = y[2 * e + 1] * c.x + y[2 * e] * c.y;
+                }
             }
-        } else {
+        } else if (KEYS) {
             // the pair's two lanes need the same NV angles: each takes half of them
             const int f0 = (upper ? d0 - half : d0);
             float2 mine[NV / 2];
@@ -320,100 +340,75 @@ __device__ void append_page(const AppendParams &P, int job, uint32_t (*amax)[kAP
                 const float2 other = make_float2(__shfl_sync(0xffffffffu, mine[e].x, partner),
                                                  __shfl_sync(0xffffffffu, mine[e].y, partner));
                 const float2 c0 = upper ? other : mine[e], c1 = upper ? mine[e] : other;   // angles e and NV / 2 + e
-                const float y0 = __shfl_sync(0xffffffffu, x[e], partner);
-                const float y1 = __shfl_sync(0xffffffffu, x[NV / 2 + e], partner);
+                const float y0 = __shfl_sync(0xffffffffu, y[e], partner);
+                const float y1 = __shfl_sync(0xffffffffu, y[NV / 2 + e], partner);
                 const float s0 = upper ? c0.y : -c0.y, s1 = upper ? c1.y : -c1.y;
-                kx[i][e] = rot ? x[e] * c0.x + y0 * s0 : x[e];
-                kx[i][NV / 2 + e] = rot ? x[NV / 2 + e] * c1.x + y1 * s1 : x[NV / 2 + e];
+                if (rot) {
+                    x[i][e] = y[e] * c0.x + y0 * s0;
+                    x[i][NV / 2 + e] = y[NV / 2 + e] * c1.x + y1 * s1;
+                }
             }
         }
-        uint32_t mk = 0, mv = 0;
+        uint32_t top = 0;
 #pragma unroll
-        for (int e = 0; e < NV; ++e) {
-            mk = max(mk, finite_abs(kx[i][e]));
-            mv = max(mv, finite_abs(e & 1 ? bf_hi(vw[i][e / 2]) : bf_lo(vw[i][e / 2])));
-        }
-        mk = __reduce_max_sync(0xffffffffu, mk);
-        mv = __reduce_max_sync(0xffffffffu, mv);
-        if (lane == 0) {   // non-negative floats order as their bits
-            atomicMax(&amax[0][(o0 + tok) / sb], mk);
-            atomicMax(&amax[1][(o0 + tok) / sb], mv);
-        }
+        for (int e = 0; e < NV; ++e) top = max(top, finite_abs(x[i][e]));
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) atomicMax(&amax[(o0 + tok) / sb], top);   // non-negative floats order as their bits
     }
-    if (a.kI) {   // index keys beside them
+    if (!KEYS && a.kI) {   // index keys beside the values
         const int nc = a.D_I / 8;
         for (int i = tid; i < m * nc; i += kAThreads) {
             const int tok = i / nc, c = (i - tok * nc) * 8;
-            const uint4 x = *reinterpret_cast<const uint4 *>(a.kI + (row0 + tok) * a.ld_kI + c);
+            const uint4 v = *reinterpret_cast<const uint4 *>(a.kI + (row0 + tok) * a.ld_kI + c);
             const int64_t o = (base + o0 + tok) * a.D_I + c;
             if (a.kI_e4m3)
-                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.kI_cache) + o) = e4m3_of8(x);
+                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.kI_cache) + o) = e4m3_of8(v);
             else
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.kI_cache) + o) = x;
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.kI_cache) + o) = v;
         }
     }
     __syncthreads();
-    // scales of the touched blocks; ratio: what the first block's earlier tokens shrink by
-    if (tid < 2) ratio[tid] = 1.f;
-    __syncthreads();
-    const int blk0 = o0 / sb, blk1 = (o0 + m - 1) / sb;
-    const int64_t sbase = base / sb;
-    for (int i = tid; i < 2 * kAPage; i += kAThreads) {
-        const int side = i / kAPage, blk = i % kAPage;
-        if (blk >= blk0 && blk <= blk1) {
-            float *ps = (side ? a.v_scale : a.k_scale) + sbase + blk;
-            float s = scale_for(__uint_as_float(amax[side][blk]));
-            if (blk * sb < o0) {   // the block holds earlier tokens
-                const float was = *ps, old = clamp_scale(was);
-                s = fmaxf(s, old);
-                ratio[side] = s == old ? 1.f : __fdiv_rn(old, s);
-            }
-            scale[side][blk] = s;
-            *ps = s;
+    if (tid <= blk1 - blk0) {   // the touched blocks' scales
+        float s = scale_for(__uint_as_float(amax[blk0 + tid]));
+        if (tid == 0 && partial) {
+            const float old = clamp_scale(was);
+            s = fmaxf(s, old);
+            if (s != old) *ratio = __fdiv_rn(old, s);   // what the earlier tokens' codes shrink by
         }
+        scale[blk0 + tid] = s;
+        scales[blk0 + tid] = s;
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         const int tok = i * NW + warp;
         if (tok >= m) break;
-        const int blk = (o0 + tok) / sb;
-        const int64_t o = (base + o0 + tok) * D;
-        store_codes<NV>(static_cast<uint8_t *>(a.k_cache) + o, lane, kx[i], scale[0][blk]);
-        float vx[NV];
-#pragma unroll
-        for (int e = 0; e < NV; ++e) vx[e] = e & 1 ? bf_hi(vw[i][e / 2]) : bf_lo(vw[i][e / 2]);
-        store_codes<NV>(static_cast<uint8_t *>(a.v_cache) + o, lane, vx, scale[1][blk]);
+        store_codes<NV>(cache + (base + o0 + tok) * D, lane, x[i], scale[(o0 + tok) / sb]);
     }
-    // earlier tokens of a block whose scale grew
-    const int words = (o0 - blk0 * sb) * (D / 4);
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-        const float f = ratio[side];
-        if (f == 1.f) continue;
-        uint32_t *w = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(side ? a.v_cache : a.k_cache) +
-                                                   (base + blk0 * sb) * D);
-        for (int i = tid; i < words; i += kAThreads) {
-            const uint32_t c = w[i];
+    const float f = *ratio;
+    if (f != 1.f) {
+        uint32_t *words = reinterpret_cast<uint32_t *>(cache + (base + blk0 * sb) * D);
+        for (int i = tid; i < (o0 - blk0 * sb) * (D / 4); i += kAThreads) {
+            const uint32_t c = words[i];
             const float2 lo = from_e4m3x2(c & 0xFFFFu), hi = from_e4m3x2(c >> 16);
-            w[i] = e4m3x2(lo.x * f, lo.y * f) | e4m3x2(hi.x * f, hi.y * f) << 16;
+            words[i] = e4m3x2(lo.x * f, lo.y * f) | e4m3x2(hi.x * f, hi.y * f) << 16;
         }
     }
 }
 
-// (The page CTAs of the 8-bit form hold a page's keys and values in registers,
-// 64 a thread; rows alone need half of that.)
 template <int D, bool INTER, bool Q8>
 __global__ void __launch_bounds__(kAThreads, Q8 ? 4 : 6) append_kernel(AppendParams P) {
     __shared__ float2 cs[kARowsMax][64];
     __shared__ int64_t slot[kARowsMax];
     __shared__ int pos[kARowsMax];
     if constexpr (Q8) {
-        if ((int)blockIdx.x < P.n_page_ctas) {
-            __shared__ uint32_t amax[2][kAPage];
-            __shared__ float scale[2][kAPage], ratio[2];
+        const int job = (int)blockIdx.x;
+        if (job < P.n_page_ctas) {
+            __shared__ uint32_t amax[kAPage];
+            __shared__ float scale[kAPage], ratio;
             __shared__ int red[4];
-            append_page<D, INTER>(P, (int)blockIdx.x, amax, scale, red, ratio);
+            if (job & 1) append_page<D, INTER, false>(P, job >> 1, amax, scale, red, &ratio);
+            else append_page<D, INTER, true>(P, job >> 1, amax, scale, red, &ratio);
             return;
         }
     }
@@ -433,7 +428,7 @@ sa_status launch_append(const AppendArgs &a, cudaStream_t st) {
     P.a = a;
     const int64_t R = (int64_t)a.B * a.T;
     P.jobs = (a.T + 62) / kAPage + 1;   // pages that T consecutive tokens can touch
-    const int64_t n_page = a.q8 ? (int64_t)a.B * P.jobs : 0;
+    const int64_t n_page = a.q8 ? 2 * (int64_t)a.B * P.jobs : 0;   // keys and values apart
     P.heads = a.q8 ? a.Hq : a.Hq + 1;
     P.u_rot = a.interleaved ? a.rot_dim / 8 : a.rot_dim / 16;
     P.u_head = P.u_rot + (a.d - a.rot_dim) / 8;
