@@ -141,8 +141,8 @@ __device__ __forceinline__ void append_rows(const AppendParams &P, int cta, floa
         if (t.h < P.heads) {
             const uint16_t *src = t.h == a.Hq ? a.k + r * a.ld_k : a.q + r * a.ld_q + t.h * a.d;
             const bool rot = t.c < P.u_rot;
-            x = *reinterpret_cast<const uint4 *>(src + (rot ? t.c * 8 : a.rot_dim + (t.c - P.u_rot) * 8));
-            if (!INTER && rot) y = *reinterpret_cast<const uint4 *>(src + half + t.c * 8);
+            x = __ldcs(reinterpret_cast<const uint4 *>(src + (rot ? t.c * 8 : a.rot_dim + (t.c - P.u_rot) * 8)));
+            if (!INTER && rot) y = __ldcs(reinterpret_cast<const uint4 *>(src + half + t.c * 8));
         } else {
             const int c = t.c * 8;
             x = c < a.d ? *reinterpret_cast<const uint4 *>(a.v + r * a.ld_v + c)
@@ -397,7 +397,7 @@ __device__ __forceinline__ void append_page(const AppendParams &P, int job, uint
 }
 
 template <int D, bool INTER, bool Q8>
-__global__ void __launch_bounds__(kAThreads, Q8 ? 4 : 6) append_kernel(AppendParams P) {
+__global__ void __launch_bounds__(kAThreads, Q8 ? 5 : 8) append_kernel(AppendParams P) {
     __shared__ float2 cs[kARowsMax][64];
     __shared__ int64_t slot[kARowsMax];
     __shared__ int pos[kARowsMax];
