@@ -66,7 +66,8 @@ struct Cfg {
     static constexpr int N2 = 2 * HQP;                    // MMA N: hi and lo columns
     static constexpr int HG = HQP == 16 ? 16 : 32;        // heads a softmax thread handles
     static constexpr int NG = HQP / HG;                   // softmax groups of 128 threads
-    static constexpr int kThreads = 128 + 128 * NG;       // loader warps, softmax warps
+    static constexpr int kThreads = 128 + 128 * NG + 32;  // loader warps, softmax warps, the MMA warp
+    static constexpr int kWarpMma = 4 + 4 * NG;
     static constexpr int kKV = kTile * D, kQ = N2 * D, kP = kTile * N2;
     static constexpr int kOffK = 0;
     // Q's parts: one after the other into the same columns of S, or with 16 heads side
@@ -92,8 +93,8 @@ struct Cfg {
     // CTAs an SM: two to four by their registers.  The loader warps hand most of
     // theirs to the softmax warps.
     static constexpr int kByRegs = HQP == 16 ? 4 : (HQP == 32 ? 3 : 2);
-    static constexpr int kRegs = HQP == 16 ? 64 : 80, kRegsLoad = 40, kRegsSoft = HQP == 16 ? 88 : (HQP == 32 ? 120 : 96);
-    static_assert(kRegsLoad * 128 + kRegsSoft * 128 * NG <= kRegs * kThreads, "registers of the launch");
+    static constexpr int kRegs = HQP == 16 ? 56 : 72, kRegsLoad = 40, kRegsSoft = HQP == 16 ? 72 : (HQP == 32 ? 104 : 88);
+    static_assert(kRegsLoad * 128 + kRegsSoft * 128 * NG + kRegs * 32 <= kRegs * kThreads, "registers of the launch");
     static_assert(kRegs * kThreads * kByRegs <= 65536, "registers of an SM");
     static constexpr int kPerSm = kSmemSm / (kSmem + 1024) < kByRegs ? kSmemSm / (kSmem + 1024) : kByRegs;
     static_assert(2 * kKV >= HQP * D * 4, "O lies in the K and V tiles when a row or its part is done");
@@ -481,35 +482,60 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                           (t == i0 && kk == 0) ? 0u : 1u);
             tc_commit(bar_pv);
         };
-        if (warp == 0 && elect_one()) issue_s(i0);
-        __syncwarp();
         bool ok = true;
         // P V(t) is phase t - i0 of its barrier; S(t) may end while some warp still looks for
         // the end of S(t - 1), so each S buffer has a barrier of its own
         auto wait_s = [&](int t) { return mbar_wait(bar_s + ((t - i0) & 1), (uint32_t)((t - i0) >> 1) & 1u, abort_flag); };
         auto wait_pv = [&](int t) { return mbar_wait(bar_pv, (uint32_t)(t - i0) & 1u, abort_flag); };
-        // Only loader warp 0 polls: warps that poll take issue slots from those that
-        // compute, and warps that wait at a barrier do not.
-        constexpr int kBarLoad = 1, kBarSoft = 6, kSoft = C::kThreads - 96;   // loader warp 0 and the softmax warps
-        if (loader) {
+        // Only the MMA warp polls: warps that poll take issue slots from those that compute,
+        // and warps that wait at a barrier do not.  It tells the loader warps when P V(t - 1) and
+        // S(t + 1) are done, and the softmax warps when P V(t - 1) is.
+        constexpr int kBarSoft = 6, kSoft = C::kThreads - 128, kBarV = 1, kBarK = 7, kLoad = 160;
+        if (warp == C::kWarpMma) {
+            // ------------------------------------------------------------ MMA warp
+            if (elect_one()) issue_s(i0);
+            __syncwarp();
+            ok = wait_s(i0);
+            bar_arrive_n(kBarSoft, kSoft);   // the first tile's scores
+            if (i0 + 1 < i1) {
+                bar_arrive_n(kBarK, kLoad);  // the K tile is free
+                bar_sync_n(kBarV, kLoad);    // K(i0 + 1) is there
+                if (elect_one()) issue_s(i0 + 1);
+                __syncwarp();
+                ok = ok && wait_s(i0 + 1);
+                bar_arrive_n(kBarK, kLoad);
+            }
+            for (int t = i0; t < i1; ++t) {
+                if (__syncthreads_or(!ok)) {   // a wait ran out: everybody leaves here
+                    bar_arrive_n(kBarSoft, kSoft);
+                    break;
+                }
+                if (elect_one()) {
+                    tc_fence_after();
+                    issue_pv(t);
+                    if (t + 2 < i1) issue_s(t + 2);
+                }
+                __syncwarp();
+                ok = wait_pv(t);
+                bar_arrive_n(kBarSoft, kSoft);
+                if (t + 1 < i1) bar_arrive_n(kBarV, kLoad);
+                if (t + 2 < i1) {
+                    ok = ok && wait_s(t + 2);
+                    bar_arrive_n(kBarK, kLoad);
+                }
+            }
+            if (!ok && lane == 0) report(A.dev_status, SA_DEV_TIMEOUT);
+        } else if (loader) {
             // ------------------------------------------------------------ loader warps
             regs_dec<C::kRegsLoad>();
             if (i0 + 1 < i1) {
-                if (warp == 0) ok = wait_s(i0);   // the K tile is free
-                bar_sync_n(kBarLoad, 128);
+                bar_sync_n(kBarK, kLoad);   // S(i0) is done: the K tile is free
                 gather(i0 + 1, A.k, C::kOffK);
                 cp_async_wait_all();
                 fence_async_smem();
-                bar_sync_n(kBarLoad, 128);
-                if (warp == 0 && elect_one()) issue_s(i0 + 1);
-                __syncwarp();
+                bar_arrive_n(kBarV, kLoad);
             }
             for (int t = i0; t < i1; ++t) {
-                // the scores of the first tile, or P V(t - 1): O and the P tile are free for the softmax
-                if (warp == 0) {
-                    ok = ok && (t == i0 ? wait_s(t) : wait_pv(t - 1));
-                    bar_arrive_n(kBarSoft, kSoft);
-                }
                 // lookups ahead: the page of tile t + 3's key, the scales of tile t + 1's
                 const int pg3 = page_of(pos3), row1 = row_of(t + 1);
                 float ks1 = 0.f, vs1 = 0.f;
@@ -518,30 +544,20 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     vs1 = __ldg(A.v_scale + (row1 >> P.sb_shift));
                 }
                 const int pos4 = position(t + 4);
-                if (warp == 0 && t + 1 < i1) ok = ok && wait_s(t + 1);   // (and the softmax of t + 1 has its scores)
-                bar_sync_n(kBarLoad, 128);
-                if (t + 2 < i1) gather(t + 2, A.k, C::kOffK);   // over K(t + 1): S(t + 1) is done
-                if (t > i0) gather(t, A.v, C::kOffV);           // over V(t - 1): P V(t - 1) is done
-                if (t + 1 < i1) put_scale(t + 1, row1, ks1, vs1);
+                if (t > i0) {
+                    bar_sync_n(kBarV, kLoad);   // P V(t - 1) is done: V(t) over V(t - 1)
+                    gather(t, A.v, C::kOffV);
+                }
+                if (t + 1 < i1) {
+                    bar_sync_n(kBarK, kLoad);   // S(t + 1) is done: K(t + 2) over K(t + 1)
+                    if (t + 2 < i1) gather(t + 2, A.k, C::kOffK);
+                    put_scale(t + 1, row1, ks1, vs1);
+                }
                 put_row(t + 3, pos3, pg3);
                 pos3 = pos4;
                 cp_async_wait_all();
                 fence_async_smem();
-                if (__syncthreads_or(!ok)) {   // a wait ran out
-                    ok = false;
-                    break;
-                }
-                if (warp == 0 && elect_one()) {
-                    tc_fence_after();
-                    issue_pv(t);
-                    if (t + 2 < i1) issue_s(t + 2);
-                }
-                __syncwarp();
-            }
-            if (warp == 0) {
-                if (ok) ok = wait_pv(i1 - 1);
-                if (!ok && lane == 0) report(A.dev_status, SA_DEV_TIMEOUT);
-                bar_arrive_n(kBarSoft, kSoft);
+                if (__syncthreads_or(false)) break;   // a wait ran out
             }
             regs_inc<C::kRegs>();
         } else {
@@ -716,10 +732,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 }
                 fence_async_smem();
                 tc_fence_before();
-                if (__syncthreads_or(!ok)) {   // a wait ran out
-                    ok = false;
-                    break;
-                }
+                if (__syncthreads_or(false)) break;   // a wait ran out
             }
             bar_sync_n(kBarSoft, kSoft);   // P V of the last tile is done
             tc_fence_after();
