@@ -634,9 +634,17 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     __syncwarp();
                 }
                 // One vote of the group a tile: does any head need a new reference?
+                // (the first 16 heads' e is kept for P, that of others read again)
+                f2 e0[8];
+                exponents(0, e0);
                 float top = -CUDART_INF_F;
 #pragma unroll
-                for (int c = 0; c < HG; c += 16) {
+                for (int i = 0; i < 8; ++i) {
+                    const float2 f = up(e0[i]);
+                    top = max3(top, f.x, f.y);
+                }
+#pragma unroll
+                for (int c = 16; c < HG; c += 16) {
                     f2 e[8];
                     exponents(c, e);
 #pragma unroll
@@ -702,6 +710,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     }
                     tmem_st_wait_all();
                     __syncwarp();
+                    exponents(0, e0);
                 }
                 // P^T as an MN-major operand without swizzle: 16-byte rows of 16 heads, the
                 // rows of 8 keys 16 bytes apart, the head chunks of a key group 128 bytes
@@ -709,7 +718,12 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
 #pragma unroll
                 for (int c = 0; c < HG; c += 16) {
                     f2 e[8];
-                    exponents(c, e);
+                    if (c == 0) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) e[i] = e0[i];
+                    } else {
+                        exponents(c, e);
+                    }
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {   // four heads
