@@ -634,7 +634,8 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     __syncwarp();
                 }
                 // One vote of the group a tile: does any head need a new reference?
-                // (the first 16 heads' e is kept for P, that of others read again)
+                // (KEEP: the first 16 heads' e is kept for P; that of others is read again)
+                constexpr bool KEEP = !CL;
                 f2 e0[8];
                 exponents(0, e0);
                 float top = -CUDART_INF_F;
@@ -660,12 +661,12 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     uint32_t heads = 0;   // those with an e above kRaise, for any key of the tile
                     if (__any_sync(0xffffffffu, top > kRaise)) {
 #pragma unroll
-                        for (int c = 0; c < HG; c += 8) {
-                            f2 e[4];
-                            exponents(c, e);
+                        for (int c = 0; c < HG; c += 16) {
+                            f2 e[8];
+                            if (c > 0 || !KEEP) exponents(c, e);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float2 f = up(e[i]);
+                            for (int i = 0; i < 8; ++i) {
+                                const float2 f = up(c > 0 || !KEEP ? e[i] : e0[i]);
                                 if (f.x > kRaise) heads |= 1u << (c + 2 * i);
                                 if (f.y > kRaise) heads |= 2u << (c + 2 * i);
                             }
@@ -679,38 +680,38 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     const uint4 fl = *reinterpret_cast<const uint4 *>(flags);
                     heads = fl.x | fl.y | fl.z | fl.w;
                     const bool mine = (heads >> lane) & 1u;
-                    float by = mine ? kStep : 0.f;
-                    if (far) {
-                        const float tm = maxima();
-                        if (mine) by = tm - kTop - m;
-                    }
+                    float to = m + kStep, f = 1.f;
+                    if (far) to = maxima() - kTop;
                     if (mine) {
-                        m += by;
+                        f = ex2f(m - to);   // what the row's earlier tiles made of the head shrinks by this
+                        m = to;
                         negm[lane] = -m;
                     }
 #pragma unroll
                     for (int c = 0; c < HG; c += 8) {
                         if (!((heads >> c) & 0xFFu)) continue;
-                        float fc[8];   // what the row's earlier tiles made of these heads shrinks
+                        float fc[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) fc[i] = ex2f(-__shfl_sync(0xffffffffu, by, c + i));
+                        for (int i = 0; i < 8; ++i) fc[i] = __shfl_sync(0xffffffffu, f, c + i);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) l[c / 2 + i] = fma2(l[c / 2 + i], pk(fc[2 * i], fc[2 * i + 1]), 0);
                         if (t > i0) {
+                            uint32_t o[8], ol[8];   // both parts
+                            tmem_ld_x8(lane_t + (uint32_t)(2 * SN + c), o);
+                            tmem_ld_x8(lane_t + (uint32_t)(2 * SN + HQP + c), ol);
+                            tmem_ld_wait();
 #pragma unroll
-                            for (int part = 0; part < 2; ++part) {
-                                uint32_t o[8];
-                                tmem_ld_x8(lane_t + (uint32_t)(2 * SN + part * HQP + c), o);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fc[k]);
-                                tmem_st8(lane_t + (uint32_t)(2 * SN + part * HQP + c), o);
+                            for (int k = 0; k < 8; ++k) {
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) * fc[k]);
+                                ol[k] = __float_as_uint(__uint_as_float(ol[k]) * fc[k]);
                             }
+                            tmem_st8(lane_t + (uint32_t)(2 * SN + c), o);
+                            tmem_st8(lane_t + (uint32_t)(2 * SN + HQP + c), ol);
                         }
                     }
                     tmem_st_wait_all();
                     __syncwarp();
-                    exponents(0, e0);
+                    if (KEEP && (heads & 0xFFFFu)) exponents(0, e0);
                 }
                 // P^T as an MN-major operand without swizzle: 16-byte rows of 16 heads, the
                 // rows of 8 keys 16 bytes apart, the head chunks of a key group 128 bytes
@@ -718,7 +719,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
 #pragma unroll
                 for (int c = 0; c < HG; c += 16) {
                     f2 e[8];
-                    if (c == 0) {
+                    if (KEEP && c == 0) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) e[i] = e0[i];
                     } else {
