@@ -50,7 +50,8 @@ namespace {
 constexpr int kTile = 128;                  // keys per tile (MMA M)
 constexpr float kTop = 1.f, kRaise = 8.75f; // log2 of a row's largest P at first, and of what it may grow to
 constexpr float kStep = 8.f;                // how far a head's reference goes up then
-constexpr float kLowest = -1e30f;           // running maximum of a row that has met no key yet
+constexpr float kLowest = -3.4028235e38f;   // running maximum of a head that has met no finite score yet
+constexpr float kCoarse = 8388608.f;        // a reference from 2^23 on is not moved by steps
 constexpr int kSmemSm = 233472;             // shared memory of an SM, 1 KB of it reserved per CTA
 
 struct Params {
@@ -142,18 +143,6 @@ __device__ __forceinline__ float redux_max(float x) {   // NaN counts as absent
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
     return r;
-}
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-    unsigned short r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)c));
-    float2 f;
-    asm("{ .reg .b16 l, u; mov.b32 {l, u}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, u; }" : "=f"(f.x), "=f"(f.y) : "r"(h));
-    return f;
 }
 __device__ __forceinline__ void cp_async16_or_zero(void *smem_dst, const void *gsrc, bool some) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(gsrc), "r"(some ? 16 : 0)
@@ -289,15 +278,15 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         if (A.lse)
             for (int i = tid; i < A.Hq; i += NT) A.lse[(int64_t)r * A.Hq + i] = -CUDART_INF_F;
     };
-    if (p < 0 && !CL) {   // a padding row
-        no_keys();
-        if (warp == 0) tmem_dealloc(*tmem_slot, C::kTmemCols);
-        return;
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);   // two S buffers (SN columns each), O (N2 columns)
+    if (p < 0 && !CL) {   // a padding row
+        no_keys();
+        if (warp == 0) tmem_dealloc(tmem, C::kTmemCols);
+        return;
+    }
 
     const int lim = p - A.W;   // top-K entries <= lim are taken; the window covers the rest
     if (p >= 0) {
@@ -574,13 +563,13 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             bool fresh = true;                         // no key yet
             bar_sync_n(kBarSoft, kSoft);               // S(i0) is done
             for (int t = i0; t < i1; ++t) {
-                // S(t) is done: loader warp 0 has waited for it
+                // S(t) is done: the MMA warp waited for it before it met the last barrier
                 tc_fence_after();
                 const uint32_t s_t = lane_t + (uint32_t)(((t - i0) & 1) * SN);
                 const float *kf = sc + (t & 1) * 3 * kTile + key;
                 const f2 c2 = pk(kf[0], kf[0]), lv2 = pk(kf[kTile], kf[kTile]), iv2 = pk(kf[2 * kTile], kf[2 * kTile]);
-                // Scores of N heads with the value's scale, in log2.  They are read from TMEM
-                // for the vote and again for P: keeping 32 of them beside 32 sums spills.
+                // Scores of N heads: read from TMEM for the vote and again for P (of 32 heads the
+                // second half: keeping all of them beside 32 sums spills).
                 auto scores = [&](int c, auto &x) {
                     constexpr int N = 2 * sizeof(x) / sizeof(f2);
                     uint32_t u[N], v[N];
@@ -600,8 +589,9 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
 #pragma unroll
                     for (int i = 0; i < N / 4; ++i) {
                         const ulonglong2 n2 = reinterpret_cast<const ulonglong2 *>(negm + c)[i];
-                        x[2 * i] = fma2(x[2 * i], c2, add2(lv2, n2.x));
-                        x[2 * i + 1] = fma2(x[2 * i + 1], c2, add2(lv2, n2.y));
+                        // (the largest one's difference to m is exact, however large both are)
+                        x[2 * i] = add2(fma2(x[2 * i], c2, lv2), n2.x);
+                        x[2 * i + 1] = add2(fma2(x[2 * i + 1], c2, lv2), n2.y);
                     }
                 };
                 // the exact maxima over the tile's keys, a head a lane
@@ -634,7 +624,8 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     __syncwarp();
                 }
                 // One vote of the group a tile: does any head need a new reference?
-                // (KEEP: the first 16 heads' e is kept for P; that of others is read again)
+                // (KEEP: the first 16 heads' e is kept for P.  2048 rows of 36 tiles: 92 us
+                // without, 88 with; the cluster form would spill.)
                 constexpr bool KEEP = !CL;
                 f2 e0[8];
                 exponents(0, e0);
@@ -675,8 +666,9 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     }
                     if (lane == 0) flags[quad] = heads;
                     // They go up by kStep: nothing but a bit a head has to be known of the other
-                    // keys.  Where that is not enough, by what takes the largest P back to 2.
-                    const bool far = bar_or(3 + 2 * hg, 128, top > kRaise + kStep);
+                    // keys.  Where that is not enough, or lost in a large reference's rounding, to
+                    // what takes the largest P back to 2.
+                    const bool far = bar_or(3 + 2 * hg, 128, top > kRaise + kStep || (lane < HG && fabsf(m) > kCoarse));
                     const uint4 fl = *reinterpret_cast<const uint4 *>(flags);
                     heads = fl.x | fl.y | fl.z | fl.w;
                     const bool mine = (heads >> lane) & 1u;

@@ -141,6 +141,30 @@ def test_append(sa, case, q8):
     check_append(x, y, T, Hq, d, D_I, rot, inter, q8, sb, kI8)
 
 
+def test_append_q8_longest_call(sa):
+    """131072 rows in one call, padded in front: every block's scale and codes."""
+    T, n, d, sb = 131072, 130_990, 64, 64
+    g = torch.Generator().manual_seed(13)
+    k = torch.randn(T, d, generator=g).mul(torch.exp2(torch.randint(-9, 9, (T, 1), generator=g).float())).bfloat16()
+    nv = ref.rows_of([n], [n], T, left=True).cuda()
+    kc, vc = (torch.full((T, d), 0x11, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.full((T // sb,), 9.0, device="cuda") for _ in range(2))
+    st, kd, vd = status_word(), k.cuda(), k.flip(1).contiguous().cuda()
+    sa.sa_cache_append_q8(None, 0, None, kd, d, vd, d, None, 0, nv, None, 0, 0, 64, T, 1, T, 0, d, 0, None, 0, 0, kc, vc, ks, vs,
+                          sb, None, 0, st)
+    assert int(st.item()) == 0
+    x = torch.zeros(T, d, dtype=torch.float64)
+    x[:n] = k[T - n:].double()
+    amax = x.view(-1, sb * d).abs().max(1).values
+    used = -(-n // sb)
+    scale = torch.tensor([ref.scale_for(float(a)) for a in amax[:used]], dtype=torch.float64)
+    assert torch.equal(ks.cpu().double()[:used], scale) and torch.equal(vs.cpu().double()[:used], scale)
+    assert (ks.cpu()[used:] == 9.0).all()
+    want = ref.to_e4m3(x[:n] / scale.repeat_interleave(sb)[:n, None])
+    assert torch.equal(kc.cpu()[:n], want) and torch.equal(vc.cpu()[:n], want.flip(1))
+    assert (kc.cpu()[n:] == 0x11).all() and (vc.cpu()[n:] == 0x11).all()
+
+
 def test_append_far_positions(sa):
     """Positions up to 2^31 - 64: the angle keeps its accuracy (the page table is short by page 0 of the pool alone)."""
     T, Hq, d, D_I = 3, 2, 128, 64
@@ -368,6 +392,37 @@ def test_attention_growing_scores_and_uneven_scales(sa, Hq, T):
     check_attention(x, got, T, K, W, sb)
 
 
+@pytest.mark.parametrize("Hq,T,order", [(16, 1, 1), (64, 160, 1), (64, 1, -1), (16, 160, -1), (33, 2, 0)])
+def test_attention_of_huge_scores(sa, Hq, T, order):
+    """Scores up to 10^9, 10^30 and 10^36 of which each is 1.2 times the next: the largest takes the whole weight, however
+    coarse fp32 is there.  Every key has the same codes, so a head's largest score is the largest or the smallest scale's."""
+    d, K, sb, L = 128, 400, 1, 400
+    for up in (-20, 50, 70):
+        x = attention_inputs([L], [T], T, Hq, d, K, 0, sb, True, seed=Hq + T)
+        g = torch.Generator().manual_seed(12)
+        x["kc"][:] = x["kc"][0].clone()
+        x["q"] = (x["q"].double() * 2.0 ** up).bfloat16()
+        step = torch.arange(L) if order > 0 else torch.arange(L).flip(0) if order < 0 else torch.randperm(L, generator=g)
+        slots = torch.tensor([ref.slot_of(x["pt"], 0, 0, p) for p in range(L)])
+        x["ks"][slots] = (2.0 ** -60 * 1.2 ** step.double()).float()
+        out, lse, st = run_attention(sa, x, T, Hq, d, K, 0, sb)
+        assert st == 0 and torch.isfinite(out).all()
+        ks, code, checked = x["ks"][slots].double(), ref.of_e4m3(x["kc"][0]), 0
+        s = (x["q"].double() @ code) * d ** -0.5   # [rows, heads]
+        for r in range(T):
+            two, at = (s[r][:, None] * ks[None, :int(x["nv"][r])]).topk(2)
+            clear = two[:, 0] - two[:, 1] > 60   # (the others are near ties: not this test's concern)
+            want = ref.of_e4m3(x["vc"][slots[at[:, 0]]]) * x["vs"][slots[at[:, 0]]].double()[:, None]
+            # P's two parts and the output's rounding, 2^-8 each, their product, fp32 sums, and e^-60 of the others
+            err = (out[r].double() - want).abs()
+            assert (err <= (2.0 ** -7 + 2.0 ** -12) * want.abs() + 1e-9)[clear].all(), (up, r)
+            # q's small values are off by 2^-18 of the largest, the fp32 score by 2^-20
+            dx = x["q"][r].double().abs().max() * 2.0 ** -18 * code.abs().sum() * d ** -0.5 * ks[at[:, 0]]
+            assert ((lse[r].double() - two[:, 0]).abs() <= dx + 2.0 ** -20 * two[:, 0].abs() + 1e-3)[clear].all(), (up, r)
+            checked += int(clear.sum())
+        assert checked > (0 if up < 70 else 0.9 * T * Hq)
+
+
 @pytest.mark.parametrize("T", [1, 150])
 def test_attention_rows_without_keys(sa, T):
     """W = 0 and rows whose top-K is empty, beside padding rows and full ones."""
@@ -586,7 +641,7 @@ def test_captured_step_replays(sa):
 
 
 def test_two_calls_at_once(sa):
-    """The same attention on two streams at once, small rows (clusters) and many rows (persistent)."""
+    """The same attention on two streams at once, few rows (clusters) and many rows (a CTA each)."""
     xs = [attention_inputs([3000] * 2, [1, 1], 1, 64, 128, 512, 64, 64, True, seed=10),
           attention_inputs([900] * 2, [180, 180], 180, 16, 128, 128, 32, 64, True, seed=11)]
     shapes = [(1, 64, 128, 512, 64, 64), (180, 16, 128, 128, 32, 64)]
