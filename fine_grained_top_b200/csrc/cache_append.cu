@@ -233,7 +233,8 @@ __device__ __forceinline__ void append_page(const AppendParams &P, int job, uint
     const int b = job / P.jobs, j = job - b * P.jobs;
     const int32_t *nv = a.n_valid + (int64_t)b * a.T;
 
-    // the sequence's run of valid rows, checked
+    // The sequence's run of valid rows, checked.  Each page reads all T numbers, from L2: next
+    // to nothing at prompt lengths, but it grows with T^2 / 64, hence the limit kAppendMaxT.
     if (tid < kAPage) amax[tid] = 0;
     if (tid == 0) *ratio = 1.f;
     int first = 0, count, err = 0, n0;   // n0: n_valid of the run's first row

@@ -140,6 +140,8 @@ inline sa_status check_decode_args(const void *q, const void *k_cache, const voi
     return SA_OK;
 }
 
+constexpr int kAppendMaxT = 131072;   // tokens a sequence and call into an 8-bit cache (see append_page)
+
 struct AppendArgs {
     const uint16_t *q, *k, *v, *kI;
     int64_t ld_q, ld_k, ld_v, ld_kI;

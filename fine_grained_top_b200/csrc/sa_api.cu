@@ -305,7 +305,7 @@ static sa_status cache_append(const sa_bf16 *q, int64_t ld_q, sa_bf16 *q_out, co
     if (kI && !(D_I == 32 || D_I == 64 || D_I == 128)) return SA_ERR_UNSUPPORTED;
     const sa_status chk = check_cache_shape(page_table, max_pages, pool_pages, page_size, S_max, B, scale_block);
     if (chk != SA_OK) return chk;
-    if ((int64_t)B * T > (1 << 30)) return SA_ERR_UNSUPPORTED;
+    if ((int64_t)B * T > (1 << 30) || (q8 && T > kAppendMaxT)) return SA_ERR_UNSUPPORTED;
     if (B == 0 || T == 0) return SA_OK;
     if (!k || !v || !k_cache || !v_cache || !n_valid || (q8 && (!k_scale || !v_scale)) || (rot_dim > 0 && !inv_freq))
         return SA_ERR_INVALID_ARG;

@@ -202,7 +202,11 @@ class KVCache:
         padding) and return the rotated queries (q [B*T, Hq, d], q_out or a new
         tensor; None when q is None)."""
         R, d = self.B * T, self.d
+        if self.paged and page_table is None:
+            raise ValueError("a paged cache is appended to through its page table")
         Hq = q.numel() // (R * d) if q is not None and R > 0 else 1
+        if q is not None and q.numel() != R * Hq * d:
+            raise ValueError("q holds whole heads of %d values for each of %d rows" % (d, R))
         if q is not None and q_out is None:
             q_out = torch.zeros((R, Hq, d), dtype=torch.bfloat16, device=q.device)
         (q, ld_q), (k, ld_k) = self._rows(q, R, Hq * d), self._rows(k, R, d)

@@ -36,7 +36,8 @@
  *   - Supported shapes: d (attention head dim) in {64, 128}; D_I (indexer
  *     dim) in {32, 64} with bf16 operands, {64, 128} with e4m3 operands and
  *     for the fused decode select; H_I in {1, 2, 4, 8} (1 .. 8 for the fused
- *     decode select); 1 <= Hq <= 64 query heads; page_size 64.  Other shapes
+ *     decode select); 1 <= Hq <= 64 query heads; page_size 64.  The cache
+ *     appends store index keys of D_I in {32, 64, 128}.  Other shapes
  *     return SA_ERR_UNSUPPORTED.  There is no fallback path.
  */
 #ifndef FINE_GRAINED_TOP_SA_H
@@ -461,7 +462,8 @@ sa_status sa_cache_append(const sa_bf16 *q, int64_t ld_q, sa_bf16 *q_out,
  *   the step's last token are left as they are.
  *   The valid rows of a sequence must be consecutive rows with consecutive
  *   positions (padding only in front or behind): otherwise SA_DEV_ORDER, and
- *   nothing of that sequence is written but its q_out rows. */
+ *   nothing of that sequence is written but its q_out rows.  T is at most
+ *   131072 (SA_ERR_UNSUPPORTED: append longer prompts in several calls). */
 sa_status sa_cache_append_q8(const sa_bf16 *q, int64_t ld_q, sa_bf16 *q_out,
                              const sa_bf16 *k, int64_t ld_k, const sa_bf16 *v,
                              int64_t ld_v, const sa_bf16 *kI, int64_t ld_kI,

@@ -62,7 +62,8 @@ def test_append_refusals(sa, kw, want, q8):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(scale_block=0), "UNSUPPORTED"), (dict(scale_block=48), "UNSUPPORTED"), (dict(scale_block=128), "UNSUPPORTED"),
-    (dict(S_max=1000), "INVALID_ARG"), (dict(k_scale=None), "INVALID_ARG"), (dict(v_scale=None), "INVALID_ARG")])
+    (dict(S_max=1000), "INVALID_ARG"), (dict(k_scale=None), "INVALID_ARG"), (dict(v_scale=None), "INVALID_ARG"),
+    (dict(T=131073), "UNSUPPORTED")])
 def test_append_q8_refusals(sa, kw, want):
     assert sa._lib.sa_cache_append_q8(*append_args(q8=True, **kw)) == getattr(sa, "SA_ERR_" + want)
 
@@ -167,3 +168,8 @@ def test_cache_and_plan_shapes():
     assert ld == 300 and tuple(q.shape) == (15, 128)
     with pytest.raises(ValueError):
         c._rows(torch.zeros(300, 15).T[:, 20:148], 15, 128)
+    new = dict(k=torch.zeros(15, 128), v=torch.zeros(15, 128), kI=torch.zeros(15, 64), n_valid=torch.zeros(15), T=5)
+    with pytest.raises(ValueError, match="page table"):
+        c.append(None, **new)
+    with pytest.raises(ValueError, match="whole heads"):
+        c.append(torch.zeros(15 * 128 + 8), page_table=torch.zeros(3, 4), **new)
