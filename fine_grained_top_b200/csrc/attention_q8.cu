@@ -22,18 +22,37 @@
 // whatever the scales), and the row sum takes P / vs.  After a raise of m the
 // largest P is 2; it may grow to 2^8.75 (e4m3 ends at 448) before the next.
 //
-// A CTA takes one row, or one run of a row's tiles (few rows: a thread-block
-// cluster shares a row, and the partial m, l, O meet through distributed shared
-// memory).  All of its warps do every step together, a tile of 128 keys at a
-// time, with one barrier of the CTA a tile:
-//   S(t) done (and with it P V(t-1)) -> copy V(t) and K(t+1) (16-byte cp.async;
-//   slots without a key are zero-filled, so nothing that was not selected is
-//   ever read) -> softmax(t) -> barrier -> one thread issues P V(t), S(t+1)
-// while the next tiles' cache rows (page table) and scales are looked up two
-// tiles and one tile ahead.  Two to five such CTAs share an SM and fill each
-// other's waits.  (A first form with one persistent CTA of 16 to 24 warps in
-// roles spent its time on instruction-cache misses and single-warp latencies:
-// 3000 to 7400 cycles a tile.)  Every wait is bounded (SA_DEV_TIMEOUT).
+// A CTA takes one row, or (few rows: the cost rule in launch_q8_rows) one run of
+// a row's tiles: a thread-block cluster shares the row, and the partial m, l, O
+// meet through distributed shared memory.  A tile is 128 keys.  The warps:
+//   4 loader warps   one key a thread looked up ahead (selection entry four tiles
+//                    ahead, page three, scales one), V(t) and K(t+2) copied with
+//                    16-byte cp.async as soon as P V(t-1) and S(t+1) let go of the
+//                    single V and K tiles (a slot without a key is zero-filled:
+//                    nothing that was not selected is ever read)
+//   4 or 8 softmax   one key a lane, 16 heads a thread with up to 16 heads, else 32
+//     warps          (two groups with 64): a vote on raises, the exponentials, P^T
+//                    into the single P tile.  32 heads keep their sums in registers
+//                    and read the scores from TMEM twice; 64 a thread spill, and 16
+//                    with four groups read each key's factors twice as often
+//   1 MMA warp       issues P V(t) and S(t+2) (two S buffers), is the only one that
+//                    polls their mbarriers, and passes each end on over a named
+//                    barrier: polling warps took issue slots from the softmax
+//                    (32 x 4 rows: 24.2 us with the loaders polling, 21.7 so)
+// and one barrier of the CTA a tile hands P(t), V(t) and the next factors over.
+// The loaders give registers to the softmax warps (setmaxnreg; without it 2048
+// rows take 119 us instead of 99), so that two (64 heads) to four CTAs share an SM and
+// fill each other's waits.  (A persistent CTA of 16 to 24 warps in roles, a row
+// after another, spent its time on instruction-cache misses and single-warp
+// latencies: 288 us for those 2048 rows.)
+//
+// What bounds it.  Few rows: the chain row start -> lookups -> gather -> S -> P ->
+// P V -> join, 1.2 us a tile, and the launch: 8 rows of 2560 keys 13.2 us, 16 paged
+// ones 17.5.  Many rows: the softmax's issue slots (about half of them busy) behind
+// the latency of a tile's chain: 2048 rows of 1152 keys and 16 heads 89 us (6.8 TB/s
+// gathered, 212 TFLOP/s), 4 x 1024 rows of up to 2560 keys and 64 heads 367 us (421
+// TFLOP/s).  Two K and V tiles, S before P V and copies of the scales by cp.async
+// changed nothing or cost 2 percent.  Every wait is bounded (SA_DEV_TIMEOUT).
 #include <math_constants.h>
 
 #include <algorithm>

@@ -10,7 +10,9 @@
 // handed to fp32 sine and cosine, so that positions far out lose nothing.
 //
 // The step is bound by its bytes (the queries of all heads make nearly all of
-// them) at prompt lengths and by one launch's latency for single tokens.
+// them) at prompt lengths, and by one launch's latency for single tokens: 8192
+// rows of 64 heads into 8 bits 55 us (5.0 TB/s), 2 x 2048 rows of 16 heads into 16
+// bits 11.7 us (3.3 TB/s), 16 single tokens 3.4 us, 64 into 16 bits 2.4 us.
 // Two kinds of CTAs share one launch:
 //   rows:  a few rows each, one 16-byte chunk (or the two halves of a pair of
 //          chunks) per thread and turn; cosines and sines once a row in shared
@@ -397,6 +399,9 @@ __device__ __forceinline__ void append_page(const AppendParams &P, int job, uint
     }
 }
 
+// CTAs an SM: the row CTAs hold two units a thread in flight, and the more CTAs
+// share an SM the better they cover each other (8192 rows of 64 heads: 92 us with the
+// two that fit unbounded, 57 with four, 55 with five; six spill).
 template <int D, bool INTER, bool Q8>
 __global__ void __launch_bounds__(kAThreads, Q8 ? 5 : 8) append_kernel(AppendParams P) {
     __shared__ float2 cs[kARowsMax][64];
