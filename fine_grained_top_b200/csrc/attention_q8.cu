@@ -76,6 +76,8 @@ constexpr int kSmemSm = 233472;             // shared memory of an SM, 1 KB of i
 struct Params {
     AttnQ8Args a;
     int G;                // CTAs a row (cluster size)
+    uint32_t inv_G;       // ceil(2^20 / G): n / G is n inv_G >> 20 for n <= 2^16 + 2^6
+    int hpr;              // heads that a CTA of a cluster joins
     int sb_shift;         // log2 of the tokens a scale
     float scale_log2;
 };
@@ -104,7 +106,7 @@ struct Cfg {
     static constexpr int kOffEpi = kOffNegM + 4 * HQP * 4;            // 1 / l, or a part's m and l [2][HQP]
     static constexpr int kOffFlags = kOffEpi + 2 * HQP * 4;  // [group][4] heads to raise, by eights
     static constexpr int kOffMisc = kOffFlags + NG * 16;
-    static constexpr int kUsed = kOffMisc + 64;
+    static constexpr int kUsed = kOffMisc + 64 + 16 * 8;
     static constexpr uint32_t kTmemCols = 2 * SN + N2 <= 64 ? 64 : (2 * SN + N2 <= 128 ? 128 : 256);   // two S buffers, O
     // CTAs wait for TMEM columns while others of their cluster wait for them, so
     // whatever shares an SM must fit its 512 columns: shared memory in proportion.
@@ -200,18 +202,29 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ float clamp_scale(float s) {   // into [2^-64, 2^64]; NaN -> 2^-64
     return fminf(fmaxf(s, 5.421010862427522e-20f), 1.8446744073709552e19f);
 }
-__device__ __forceinline__ float dsmem_ld_f32(const void *local, uint32_t rank) {
-    return __uint_as_float(dsmem_ld_u32(local, rank));
-}
-__device__ __forceinline__ float4 dsmem_ld_f4(const void *local, uint32_t rank) {
+// The address of this CTA's shared memory `local` in CTA `rank` of the cluster, and loads from such.
+__device__ __forceinline__ uint32_t in_cta(const void *local, uint32_t rank) {
     uint32_t remote;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
+    return remote;
+}
+__device__ __forceinline__ float2 dsmem_ld_f2(uint32_t at) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 dsmem_ld_f4(uint32_t at) {
     float4 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(remote)
+                 : "r"(at)
                  : "memory");
     return v;
+}
+__device__ __forceinline__ uint32_t cluster_id() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+    return r;
 }
 // Byte offset of 16-byte chunk `ch` of row `r` in a tile of D-byte rows with
 // the D-byte swizzle (128 or 64).
@@ -241,25 +254,63 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     extern __shared__ __align__(1024) uint8_t sm[];   // (no static shared memory: it begins 1024-byte aligned)
     int32_t *rows = reinterpret_cast<int32_t *>(sm + C::kOffRows);
     float *sc = reinterpret_cast<float *>(sm + C::kOffSc);
-    float *epi = reinterpret_cast<float *>(sm + C::kOffEpi), *epi_l = epi + HQP;   // 1 / l, or a part's m and l
+    float *epi = reinterpret_cast<float *>(sm + C::kOffEpi);         // a row's 1 / l,
+    float2 *part_ml = reinterpret_cast<float2 *>(sm + C::kOffEpi);   // or its part's m and l
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + C::kOffMisc);
     uint64_t *bar_s = bar, *bar_pv = bar + 2;   // S(t) done, one for each S buffer; P V(t) done
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 3);
     int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
-    unsigned *s_first = reinterpret_cast<unsigned *>(tmem_slot + 2), *s_qmax = s_first + 1, *s_qodd = s_first + 2;
+    uint2 *found = reinterpret_cast<uint2 *>(sm + C::kOffMisc + 64);   // a warp's first entry not taken, its largest |q|
 
     const AttnQ8Args &A = P.a;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int G = CL ? P.G : 1, rank = CL ? (int)cluster_rank() : 0;
-    const int r = CL ? (int)blockIdx.x / G : (int)blockIdx.x, b = r / A.T;
+    const int r = CL ? (int)cluster_id() : (int)blockIdx.x, b = A.T == 1 ? r : r / A.T;
+    auto by_G = [&](int n) { return CL ? (int)(((uint64_t)n * P.inv_G) >> 20) : n; };   // n / G
 
     // ------------------------------------------------------------ the row
-    // What does not depend on anything goes first: its length and its Q (16 dims a
-    // thread and turn).
+    // Loads that wait for nothing go first: its length, its Q (16 dims a thread and turn),
+    // the start of its top-K row (16 bytes a thread and turn), and the selection's entries
+    // of this CTA's first three tiles if the top-K row is full, as most are.  The pages of
+    // those follow as soon as the length is there.  (Each after the barrier that makes it
+    // certain: 32 x 4 rows 21.9 us instead of 21.0, 3 x 37 small ones 6.4 instead of 6.0.
+    // The second turn over the top-K row pays with the longer rows that go with 64 heads:
+    // 8 rows of 2560 keys 13.4 us without it, 13.0 with; 2048 rows of 16 heads 88 and 91.)
     const int nv = __ldg(A.n_valid + r);
     const int32_t *trow = A.topk + (int64_t)r * A.K;
+    const int32_t *pt = A.page_table ? A.page_table + (int64_t)b * A.max_pages : nullptr;
+    const bool loader = warp < 4;
     constexpr int CPH = D / 16;   // 16-dim chunks of a head
     constexpr int NQ = (HQP * CPH + NT - 1) / NT;   // chunks a thread
+    constexpr int NE = HQP == 64 ? 2 : 1, NP = 3;   // turns over the top-K row that go first, tiles looked up
+    const bool vec = (A.K & 3) == 0 && (reinterpret_cast<uintptr_t>(A.topk) & 15u) == 0;
+    auto entries = [&](int k) {   // k .. k + 3 of the top-K row
+        int4 v = make_int4(-1, -1, -1, -1);
+        if (vec) {
+            if (k < A.K) v = __ldg(reinterpret_cast<const int4 *>(trow + k));
+        } else {
+            if (k < A.K) v.x = __ldg(trow + k);
+            if (k + 1 < A.K) v.y = __ldg(trow + k + 1);
+            if (k + 2 < A.K) v.z = __ldg(trow + k + 2);
+            if (k + 3 < A.K) v.w = __ldg(trow + k + 3);
+        }
+        return v;
+    };
+    auto entry_before = [&](int k) { return lane == 0 && k > 0 && k <= A.K ? __ldg(trow + k - 1) : -1; };   // (others ask their neighbour)
+    int4 ent[NE];
+    int before[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        ent[i] = entries(4 * (tid + i * NT));
+        before[i] = entry_before(4 * (tid + i * NT));
+    }
+    const int g0 = by_G((A.K + A.W + kTile - 1) / kTile * rank);   // this CTA's first tile, if so
+    int pos_g[NP], page_g[NP];
+#pragma unroll
+    for (int t = 0; t < NP; ++t) {
+        const int kk = (g0 + t) * kTile + tid;
+        pos_g[t] = loader && kk < A.K ? __ldg(trow + kk) : -1;
+    }
     uint4 qv[2 * NQ];
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
@@ -276,15 +327,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         mbar_init(bar_s + 1, 1);
         mbar_init(bar_pv, 1);
         *abort_flag = 0;
-        *s_first = (unsigned)A.K;
-        *s_qmax = 0;
-        *s_qodd = 0;
         fence_mbar_init();
-    }
-    if (warp == 0) {
-        tmem_alloc(tmem_slot, C::kTmemCols);
-        tmem_relinquish();
-        __syncwarp();
     }
     int p = nv - 1;
     if (nv < 0 || nv > A.S_max) {
@@ -297,69 +340,74 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         if (A.lse)
             for (int i = tid; i < A.Hq; i += NT) A.lse[(int64_t)r * A.Hq + i] = -CUDART_INF_F;
     };
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);   // two S buffers (SN columns each), O (N2 columns)
     if (p < 0 && !CL) {   // a padding row
         no_keys();
-        if (warp == 0) tmem_dealloc(tmem, C::kTmemCols);
         return;
+    }
+    if (warp == C::kWarpMma) {
+        tmem_alloc(tmem_slot, C::kTmemCols);
+        tmem_relinquish();
+    }
+    const int w0 = max(0, p - A.W + 1);
+#pragma unroll
+    for (int t = 0; t < NP; ++t) {
+        const int kk = (g0 + t) * kTile + tid;
+        if (kk >= A.K) pos_g[t] = w0 + (kk - A.K);
+        page_g[t] = loader && pt && pos_g[t] >= 0 && pos_g[t] <= p ? __ldg(pt + (pos_g[t] >> 6)) : 0;
     }
 
     const int lim = p - A.W;   // top-K entries <= lim are taken; the window covers the rest
     if (p >= 0) {
         int first_out = A.K;
         bool bad_idx = false, bad_ord = false;
-        const bool vec = (A.K & 3) == 0 && (reinterpret_cast<uintptr_t>(A.topk) & 15u) == 0;
-        for (int k = 4 * tid; k < A.K; k += 4 * NT) {
+        auto check = [&](int k, const int4 &v, int first) {
             int e[5];   // entries k - 1 .. k + 3
-            e[0] = k > 0 ? __ldg(trow + k - 1) : -1;
-            if (vec) {
-                const int4 v = __ldg(reinterpret_cast<const int4 *>(trow + k));
-                e[1] = v.x; e[2] = v.y; e[3] = v.z; e[4] = v.w;
-            } else {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) e[u + 1] = k + u < A.K ? __ldg(trow + k + u) : -1;
-            }
+            e[0] = __shfl_up_sync(0xffffffffu, v.w, 1);
+            if (lane == 0) e[0] = first;
+            e[1] = v.x; e[2] = v.y; e[3] = v.z; e[4] = v.w;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 if (e[u + 1] > p) bad_idx = true;
                 if (e[u + 1] >= 0 && k + u > 0 && !(e[u] >= 0 && e[u] < e[u + 1])) bad_ord = true;
                 if (!(e[u + 1] >= 0 && e[u + 1] <= lim)) first_out = min(first_out, k + u);
             }
-        }
+        };
+#pragma unroll
+        for (int i = 0; i < NE; ++i) check(4 * (tid + i * NT), ent[i], before[i]);
+        for (int k = 4 * (tid + NE * NT); k - 4 * lane < A.K; k += 4 * NT) check(k, entries(k), entry_before(k));   // (whole warps)
         if (rank == 0 && bad_idx) report(A.dev_status, SA_DEV_INDEX);
         if (rank == 0 && bad_ord) report(A.dev_status, SA_DEV_ORDER);
         first_out = (int)__reduce_min_sync(0xffffffffu, (unsigned)first_out);
-        uint32_t mx = 0, odd = 0;   // largest finite |q|; any infinite or NaN
+        auto largest_q = [&](uint32_t below) {   // |q| in bf16 bits; `below`: of those under it
+            uint32_t mx = 0;
 #pragma unroll
-        for (int i = 0; i < 2 * NQ; ++i) {
-            const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+            for (int i = 0; i < 2 * NQ; ++i) {
+                const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t t = w[k] & 0x7FFF7FFFu;
-                const uint32_t fin = __vcmpltu2(t, 0x7F807F80u);
-                mx = __vmaxu2(mx, t & fin);
-                odd |= ~fin;
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t t = w[k] & 0x7FFF7FFFu;
+                    if (below) t &= __vcmpltu2(t, below);
+                    mx = __vmaxu2(mx, t);
+                }
             }
-        }
-        mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
-        if (lane == 0) {
-            atomicMin(s_first, (unsigned)first_out);
-            atomicMax(s_qmax, mx);
-        }
-        if (odd) *s_qodd = 1;
+            return __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
+        };
+        uint32_t mx = largest_q(0), odd = mx >= 0x7F80u;
+        if (odd) mx = largest_q(0x7F807F80u);   // an infinite or NaN one: the largest finite
+        if (lane == 0) found[warp] = make_uint2((unsigned)first_out, mx | odd << 16);
     }
+    tc_fence_before();
     __syncthreads();
-    const int n_top = p >= 0 ? (int)*s_first : 0;
-    const int w0 = max(0, p - A.W + 1);
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);   // two S buffers (SN columns each), O (N2 columns)
+    const uint2 part = found[min(lane, NT / 32 - 1)];
+    const int n_top = p >= 0 ? (int)__reduce_min_sync(0xffffffffu, part.x) : 0;
+    const uint32_t q_max = __reduce_max_sync(0xffffffffu, part.y & 0xFFFFu), q_odd = __any_sync(0xffffffffu, part.y >> 16);
     const int n_keys = p >= 0 ? n_top + (p - w0 + 1) : 0;
     const int n_tiles = (n_keys + kTile - 1) / kTile;
-    const int i0 = (int)((int64_t)n_tiles * rank / G), i1 = (int)((int64_t)n_tiles * (rank + 1) / G);
+    const int i0 = by_G(n_tiles * rank), i1 = by_G(n_tiles * (rank + 1));
     if (n_keys == 0 && rank == 0) no_keys();
 
-    const bool loader = warp < 4;
     // softmax warps: TMEM lane quadrant, group, first head
     const int quad = warp & 3, hg = loader ? 0 : (warp >> 2) - 1, h0 = hg * HG;
     const int key = quad * 32 + lane;                     // TMEM lane: key (S^T) or head dim (O^T)
@@ -367,16 +415,14 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     float *negm = reinterpret_cast<float *>(sm + C::kOffNegM) + (hg * 4 + quad) * HG;   // this warp's copy
 
     if (i0 < i1) {
-        // the largest value's power of two, so that it lies in (224, 448]; at least 2^-120
-        int ex;
-        const float amax = __uint_as_float(*s_qmax << 16), mant = frexpf(amax, &ex);
-        const int e2 = amax > 0.f ? max(-120, mant <= 0.875f ? ex - 9 : ex - 8) : 0;
+        // the largest value's power of two, so that it lies in (224, 448] (a mantissa beyond
+        // 1.75 carries into the exponent); at least 2^-120
+        const int e2 = max(-120, (int)(((q_max << 16) + 0x1FFFFFu) >> 23) - 135);
         const float down = __int_as_float((127 - e2) << 23);
         const float factor = __int_as_float((e2 + 127) << 23) * P.scale_log2;
 
         constexpr int RPT = 128 / CPH, NIT = kTile / RPT;   // rows that the loader threads copy at once, turns
         // lookups of the loader threads, one key each: position (-1: none), page, cache row, scales
-        const int32_t *pt = A.page_table ? A.page_table + (int64_t)b * A.max_pages : nullptr;
         auto position = [&](int t) {
             const int kk = t * kTile + tid;
             return t < i1 && kk < n_keys ? (kk < n_top ? __ldg(trow + kk) : w0 + (kk - n_top)) : -1;
@@ -402,12 +448,16 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         };
         int pos3 = -1;   // the position of tile t + 3's key
         if (loader) {
-            const int pos0 = position(i0), pos1 = position(i0 + 1), pos2 = position(i0 + 2);
-            const int pg0 = page_of(pos0), pg1 = page_of(pos1), pg2 = page_of(pos2);
+            if (n_top != A.K || i0 != g0) {   // it came otherwise
+#pragma unroll
+                for (int t = 0; t < NP; ++t) pos_g[t] = position(i0 + t);
+#pragma unroll
+                for (int t = 0; t < NP; ++t) page_g[t] = page_of(pos_g[t]);
+            }
             pos3 = position(i0 + 3);
-            put_row(i0, pos0, pg0);
-            put_row(i0 + 1, pos1, pg1);
-            put_row(i0 + 2, pos2, pg2);
+#pragma unroll
+            for (int t = 0; t < NP; ++t)
+                put_row(i0 + t, i0 + t < i1 && (i0 + t) * kTile + tid < n_keys ? pos_g[t] : -1, page_g[t]);
         }
         __syncthreads();
 
@@ -453,7 +503,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 hi[k] = e4m3x4_of_f16(y[0], y[1]);
                 f16_of_e4m3x4(hi[k], h[0], h[1]);
                 lo[k] = e4m3x4_of_f16(hsub2(y[0], h[0]), hsub2(y[1], h[1]));
-                if (*s_qodd) {   // an infinite q makes NaN scores, as the formula does
+                if (q_odd) {   // an infinite q makes NaN scores, as the formula does
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (((w[2 * k + j / 2] >> (16 * (j & 1))) & 0x7F80u) == 0x7F80u) hi[k] |= 0x7Fu << (8 * j);
@@ -788,8 +838,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 const float L = (gmax[lane] + gmax[HG + lane]) + (gmax[2 * HG + lane] + gmax[3 * HG + lane]);
                 const int h = h0 + lane;
                 if (CL) {
-                    epi[h] = m;
-                    epi_l[h] = L;
+                    part_ml[h] = make_float2(m, L);
                 } else {
                     epi[h] = L == 0.f ? 0.f : 1.f / L;
                     if (A.lse && h < A.Hq)
@@ -829,12 +878,11 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             regs_dec<C::kRegs>();
         }
     } else if (CL && tid < HQP) {   // no share of the row
-        epi[tid] = kLowest;
-        epi_l[tid] = 0.f;
+        part_ml[tid] = make_float2(kLowest, 0.f);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == C::kWarpMma) {
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmemCols);
     }
@@ -842,22 +890,24 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         // join the parts of the heads rank * hpr ..: 4 dims a thread, four threads of which
         // each takes every fourth part, all of its loads in flight at once
         cluster_sync();
-        const int hpr = (A.Hq + G - 1) / G, hb = rank * hpr, nh = n_keys > 0 ? max(0, min(hpr, A.Hq - hb)) : 0;
-        const float *part = reinterpret_cast<const float *>(sm + C::kOffK);
-        const int n = nh * D;
+        const int hb = rank * P.hpr, nh = n_keys > 0 ? max(0, min(P.hpr, A.Hq - hb)) : 0;
+        const int n = nh * D, cq = tid & 3;
+        uint32_t there[4];   // the shared memory of this thread's parts
+#pragma unroll
+        for (int u = 0; u < 4; ++u) there[u] = in_cta(sm, (uint32_t)min(cq + 4 * u, G - 1));
         for (int i = tid; i < (n + 31) / 32 * 32; i += NT) {   // whole warps
-            const int ii = min(i, n - 1), cq = ii & 3, d4 = (ii >> 2) % (D / 4), h = (ii >> 2) / (D / 4);
+            const int ii = min(i, n - 1) >> 2, d4 = ii % (D / 4), h = ii / (D / 4);
             float mc[4], lc[4];
             float4 vc[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int c = cq + 4 * u;
                 mc[u] = kLowest;
                 lc[u] = 0.f;
-                if (c < G) {
-                    mc[u] = dsmem_ld_f32(epi + hb + h, (uint32_t)c);
-                    lc[u] = dsmem_ld_f32(epi_l + hb + h, (uint32_t)c);
-                    vc[u] = dsmem_ld_f4(part + (hb + h) * D + 4 * d4, (uint32_t)c);
+                if (cq + 4 * u < G) {
+                    const float2 ml = dsmem_ld_f2(there[u] + C::kOffEpi + (hb + h) * 8);
+                    mc[u] = ml.x;
+                    lc[u] = ml.y;
+                    vc[u] = dsmem_ld_f4(there[u] + C::kOffK + ((hb + h) * D + 4 * d4) * 4);
                 }
             }
             float m = kLowest, L = 0.f;
@@ -982,6 +1032,8 @@ sa_status launch_q8_rows(const AttnQ8Args &a, cudaStream_t st) {
             p.G = G;
         }
     }
+    p.inv_G = ((1u << 20) + p.G - 1) / p.G;
+    p.hpr = (a.Hq + p.G - 1) / p.G;
     p.sb_shift = 0;
     while ((1 << p.sb_shift) < a.scale_block) ++p.sb_shift;
     p.scale_log2 = a.scale * 1.4426950408889634f;
