@@ -12,14 +12,15 @@
 // The step is bound by its bytes (the queries of all heads make nearly all of
 // them) at prompt lengths, and by one launch's latency for single tokens: 8192
 // rows of 64 heads into 8 bits 55 us (5.0 TB/s), 2 x 2048 rows of 16 heads into 16
-// bits 11.7 us (3.3 TB/s), 16 single tokens 3.4 us, 64 into 16 bits 2.4 us.
+// bits 11.6 us (3.3 TB/s), 16 single tokens 3.4 us, 64 into 16 bits 2.4 us, 7 x 333
+// ragged rows with blocks of 16 into 8 bits 5.3 us.
 // Two kinds of CTAs share one launch:
 //   rows:  a few rows each, one 16-byte chunk (or the two halves of a pair of
 //          chunks) per thread and turn; cosines and sines once a row in shared
 //          memory, used by all of its heads.  With a 16-bit cache the key is one
 //          more head of the row, value and index key are copied beside it.
-//   pages: (8-bit caches) the new keys or values of one 64-token page, so that
-//          every scale block has one owner whatever its length: a warp holds a
+//   pages: (8-bit caches) the new keys or values of one 64-token page, or of a
+//          part of one, so that every scale block has one owner: a warp holds a
 //          token in registers (d / 32 values a lane, pair partners exchanged by
 //          shuffles), block maxima meet in shared memory, and codes are made
 //          from the registers once the scales are known.
@@ -39,7 +40,8 @@ constexpr int kAPage = 64;
 struct AppendParams {
     AppendArgs a;
     int n_page_ctas;     // CTAs of the page kind, first in the grid (8-bit caches)
-    int jobs;            // pages a sequence
+    int unit;            // tokens of a page CTA: a page, or a part of one that whole scale blocks make
+    int jobs;            // such units a sequence
     int rows;            // rows per row CTA
     int heads;           // heads a row CTA rotates: Hq, and the key with a 16-bit cache
     int u_rot, u_head;   // rotating chunks (or chunk pairs) and all units of a head
@@ -226,7 +228,7 @@ __device__ __forceinline__ uint32_t finite_abs(float x) {   // bits of |x|, 0 fo
     return b < 0x7F800000u ? b : 0u;
 }
 
-// One side of a page: its new keys (rotated) or values.
+// One side of a page, or of a part of it: its new keys (rotated) or values.
 template <int D, bool INTER, bool KEYS>
 __device__ __forceinline__ void append_page(const AppendParams &P, int job, uint32_t *amax, float *scale, int *red, float *ratio) {
     constexpr int NV = D / 32, NW = kAThreads / 32, NT = kAPage / NW;   // values a lane, warps, tokens a warp
@@ -235,7 +237,7 @@ __device__ __forceinline__ void append_page(const AppendParams &P, int job, uint
     const int b = job / P.jobs, j = job - b * P.jobs;
     const int32_t *nv = a.n_valid + (int64_t)b * a.T;
 
-    // The sequence's run of valid rows, checked.  Each page reads all T numbers, from L2: next
+    // The sequence's run of valid rows, checked.  Each unit reads all T numbers, from L2: next
     // to nothing at prompt lengths, but it grows with T^2 / 64, hence the limit kAppendMaxT.
     if (tid < kAPage) amax[tid] = 0;
     if (tid == 0) *ratio = 1.f;
@@ -280,12 +282,12 @@ __device__ __forceinline__ void append_page(const AppendParams &P, int job, uint
         if (err && j == 0 && tid == 0) report(a.dev_status, err);
         return;
     }
-    const int p0 = n0 - 1, page = p0 / kAPage + j;
-    const int begin = max(p0, page * kAPage), m = min(p0 + count, (page + 1) * kAPage) - begin;
+    const int p0 = n0 - 1, o_p0 = p0 & (P.unit - 1);   // first position, its place in its unit
+    const int at = max(j * P.unit - o_p0, 0), m = min((j + 1) * P.unit - o_p0, count) - at;   // the unit's tokens of the run
     if (m <= 0) return;
-    const int64_t base = cache_slot(a, b, page * kAPage);   // the page's first slot
-    const int o0 = begin % kAPage, sb = a.scale_block;
-    const int64_t row0 = (int64_t)b * a.T + first + (begin - p0);
+    const int begin = p0 + at, o0 = begin & (P.unit - 1), sb = a.scale_block;
+    const int64_t base = cache_slot(a, b, begin - o0);   // the unit's first slot
+    const int64_t row0 = (int64_t)b * a.T + first + at;
     const uint16_t *src = KEYS ? a.k : a.v;
     const int64_t ld = KEYS ? a.ld_k : a.ld_v;
     uint8_t *cache = static_cast<uint8_t *>(KEYS ? a.k_cache : a.v_cache);
@@ -433,7 +435,11 @@ sa_status launch_append(const AppendArgs &a, cudaStream_t st) {
     AppendParams P;
     P.a = a;
     const int64_t R = (int64_t)a.B * a.T;
-    P.jobs = (a.T + 62) / kAPage + 1;   // pages that T consecutive tokens can touch
+    // Smaller units shorten a page CTA's chain, but each reads all T lengths.  Blocks of 16,
+    // one sequence, units of 16 / 32 / 64 tokens: 64 rows 4.1 / 5.1 / 6.9 us, 1024 rows 5.0 /
+    // 5.4 / 7.0, 4096 rows 8.7 / 8.0 / 9.3, 16384 rows 42 / 28 / 23.
+    P.unit = a.T <= 1024 ? std::max(a.scale_block, 16) : a.T <= 4096 ? std::max(a.scale_block, 32) : kAPage;
+    P.jobs = (a.T + P.unit - 2) / P.unit + 1;   // units that T consecutive tokens can touch
     const int64_t n_page = a.q8 ? 2 * (int64_t)a.B * P.jobs : 0;   // keys and values apart
     P.heads = a.q8 ? a.Hq : a.Hq + 1;
     P.u_rot = a.interleaved ? a.rot_dim / 8 : a.rot_dim / 16;
