@@ -189,6 +189,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {   // NaN coun
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -372,9 +377,18 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 if (!(e[u + 1] >= 0 && e[u + 1] <= lim)) first_out = min(first_out, k + u);
             }
         };
+        for (int k = 4 * tid;;) {
+            check(k, ent[0], before[0]);
+            k += 4 * NT;
+            if (k - 4 * lane >= A.K) break;   // (whole warps)
 #pragma unroll
-        for (int i = 0; i < NE; ++i) check(4 * (tid + i * NT), ent[i], before[i]);
-        for (int k = 4 * (tid + NE * NT); k - 4 * lane < A.K; k += 4 * NT) check(k, entries(k), entry_before(k));   // (whole warps)
+            for (int i = 0; i + 1 < NE; ++i) {
+                ent[i] = ent[i + 1];
+                before[i] = before[i + 1];
+            }
+            ent[NE - 1] = entries(k + 4 * (NE - 1) * NT);
+            before[NE - 1] = entry_before(k + 4 * (NE - 1) * NT);
+        }
         if (rank == 0 && bad_idx) report(A.dev_status, SA_DEV_INDEX);
         if (rank == 0 && bad_ord) report(A.dev_status, SA_DEV_ORDER);
         first_out = (int)__reduce_min_sync(0xffffffffu, (unsigned)first_out);
@@ -444,7 +458,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             float *o = sc + (t & 1) * 3 * kTile + tid;
             o[0] = row >= 0 ? clamp_scale(ks) * factor : 0.f;
             o[kTile] = row >= 0 ? __log2f(vs) : -CUDART_INF_F;
-            o[2 * kTile] = row >= 0 ? __frcp_rn(vs) : 0.f;
+            o[2 * kTile] = row >= 0 ? rcp(vs) : 0.f;
         };
         int pos3 = -1;   // the position of tile t + 3's key
         if (loader) {
@@ -840,7 +854,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 if (CL) {
                     part_ml[h] = make_float2(m, L);
                 } else {
-                    epi[h] = L == 0.f ? 0.f : 1.f / L;
+                    epi[h] = L == 0.f ? 0.f : rcp(L);
                     if (A.lse && h < A.Hq)
                         A.lse[(int64_t)r * A.Hq + h] = L == 0.f ? -CUDART_INF_F : (m + log2f(L)) * 0.69314718055994531f;
                 }
@@ -881,7 +895,8 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         part_ml[tid] = make_float2(kLowest, 0.f);
     }
     tc_fence_before();
-    __syncthreads();
+    if (CL) cluster_sync();
+    else __syncthreads();
     if (warp == C::kWarpMma) {
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmemCols);
@@ -889,7 +904,6 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     if (CL) {
         // join the parts of the heads rank * hpr ..: 4 dims a thread, four threads of which
         // each takes every fourth part, all of its loads in flight at once
-        cluster_sync();
         const int hb = rank * P.hpr, nh = n_keys > 0 ? max(0, min(P.hpr, A.Hq - hb)) : 0;
         const int n = nh * D, cq = tid & 3;
         uint32_t there[4];   // the shared memory of this thread's parts
@@ -934,7 +948,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 o.w += __shfl_xor_sync(0xffffffffu, o.w, k);
             }
             if (cq == 0 && i < n) {
-                const float s = L == 0.f ? 0.f : 1.f / L;
+                const float s = L == 0.f ? 0.f : rcp(L);
                 uint2 ob;
                 ob.x = pack_bf16(o.x * s, o.y * s);
                 ob.y = pack_bf16(o.z * s, o.w * s);
