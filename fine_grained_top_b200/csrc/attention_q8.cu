@@ -1025,12 +1025,12 @@ sa_status launch_q8_rows(const AttnQ8Args &a, cudaStream_t st) {
     p.a = a;
     const int R = a.B * a.T;
     const int tiles = (int)std::min<int64_t>(((int64_t)a.K + a.W + kTile - 1) / kTile, ((int64_t)a.S_max + kTile - 1) / kTile);
-    // CTAs a row.  In units of one tile's time in a cluster (1.2 us with 16 heads, 1.8
-    // with 64), alone on an SM, a cluster takes 6 for its row's start and join and 1 a
-    // tile, a single CTA 4.7 and 0.9; another CTA on the SM costs all of them 28 percent
-    // with up to 32 heads, 42 with 64 (fitted to rows of 4 to 40 tiles, 1 to 300 rows:
-    // 8 rows of 20 tiles and 64 heads 13.9 us with 10 CTAs a row, 38 with one, 18 with 16;
-    // 100 such rows 46 us with one, 50 with 4).
+    // CTAs a row.  In units of one tile's time in a cluster (1.0 us with 16 heads, 1.9
+    // with 64), alone on an SM, a cluster takes 5.4 for its row's start and join and 1 a
+    // tile, a single CTA 3.2 and 0.85; another CTA on the SM costs all of them 24 percent
+    // with up to 32 heads, 33 with 64 (fitted to rows of 4 to 40 tiles, 1 to 300 rows, where
+    // it is 1 percent off the best on average: 8 rows of 20 tiles and 64 heads 12.0 us with
+    // 10 CTAs a row, 36.7 with one, 15.8 with 16; 100 such rows 41.4 us with one, 43.4 with 4).
     p.G = 1;
     double best = 0;
     if (prepare_kernel<attn_q8_kernel<D, HQP, true>>(C::kSmem, true) != cudaSuccess) return SA_ERR_CUDA;
@@ -1039,7 +1039,7 @@ sa_status launch_q8_rows(const AttnQ8Args &a, cudaStream_t st) {
         const int at_once = active_clusters<D, HQP>(dev, sms, G);
         if (at_once < 1) continue;
         const int n = (R + at_once - 1) / at_once, t = (tiles + G - 1) / G;
-        const double cost = (G == 1 ? 4.7 + 0.9 * t : 6.0 + t) * (1.0 + (HQP == 64 ? 0.42 : 0.28) * (std::min(n, C::kPerSm) - 1)) *
+        const double cost = (G == 1 ? 3.2 + 0.85 * t : 5.4 + t) * (1.0 + (HQP == 64 ? 0.33 : 0.24) * (std::min(n, C::kPerSm) - 1)) *
                             ((n + C::kPerSm - 1) / C::kPerSm);
         if (G == 1 || cost < best) {
             best = cost;
