@@ -213,18 +213,14 @@ __device__ __forceinline__ uint32_t in_cta(const void *local, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
     return remote;
 }
-__device__ __forceinline__ float2 dsmem_ld_f2(uint32_t at) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
-    return v;
+__device__ __forceinline__ void dsmem_ld(uint32_t at, float (&v)[2]) {
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(at) : "memory");
 }
-__device__ __forceinline__ float4 dsmem_ld_f4(uint32_t at) {
-    float4 v;
+__device__ __forceinline__ void dsmem_ld(uint32_t at, float (&v)[4]) {
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
                  : "r"(at)
                  : "memory");
-    return v;
 }
 __device__ __forceinline__ uint32_t cluster_id() {
     uint32_t r;
@@ -902,60 +898,45 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         tmem_dealloc(tmem, C::kTmemCols);
     }
     if (CL) {
-        // join the parts of the heads rank * hpr ..: 4 dims a thread, four threads of which
-        // each takes every fourth part, all of its loads in flight at once
+        // Join the parts of the heads rank * hpr ..: a warp a head, D / 32 dims a lane, so that a
+        // load takes a whole row of one CTA's memory.  (16 paged rows of 2560 keys and 64 heads
+        // 15.1 us; with each lane of four taking every fourth part of 4 dims, so that a load went
+        // to four CTAs, 16.1.)
+        constexpr int V = D / 32, AT = 10;   // dims a lane, parts on their way at once
         const int hb = rank * P.hpr, nh = n_keys > 0 ? max(0, min(P.hpr, A.Hq - hb)) : 0;
-        const int n = nh * D, cq = tid & 3;
-        uint32_t there[4];   // the shared memory of this thread's parts
+        for (int h = hb + warp; h < hb + nh; h += NT / 32) {
+            float v[AT][V];
+            const uint32_t off = C::kOffK + (h * D + lane * V) * 4;
+            auto fetch = [&](int c0) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) there[u] = in_cta(sm, (uint32_t)min(cq + 4 * u, G - 1));
-        for (int i = tid; i < (n + 31) / 32 * 32; i += NT) {   // whole warps
-            const int ii = min(i, n - 1) >> 2, d4 = ii % (D / 4), h = ii / (D / 4);
-            float mc[4], lc[4];
-            float4 vc[4];
+                for (int u = 0; u < AT; ++u)
+                    if (c0 + u < G) dsmem_ld(in_cta(sm, (uint32_t)(c0 + u)) + off, v[u]);
+            };
+            float ml[2] = {kLowest, 0.f};   // part `lane`: its reference and sum
+            if (lane < G) dsmem_ld(in_cta(sm, (uint32_t)lane) + C::kOffEpi + h * 8, ml);
+            fetch(0);
+            const bool some = ml[1] != 0.f;   // (a part without keys wrote nothing)
+            const float m = redux_max(some ? ml[0] : kLowest), f = some ? ex2f(ml[0] - m) : 0.f;
+            float L = some ? f * ml[1] : 0.f;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                mc[u] = kLowest;
-                lc[u] = 0.f;
-                if (cq + 4 * u < G) {
-                    const float2 ml = dsmem_ld_f2(there[u] + C::kOffEpi + (hb + h) * 8);
-                    mc[u] = ml.x;
-                    lc[u] = ml.y;
-                    vc[u] = dsmem_ld_f4(there[u] + C::kOffK + ((hb + h) * D + 4 * d4) * 4);
+            for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+            const float w = L == 0.f ? 0.f : f * rcp(L);
+            float o[V] = {};
+            for (int c0 = 0; c0 < G; c0 += AT) {
+                if (c0 > 0) fetch(c0);
+#pragma unroll
+                for (int u = 0; u < AT; ++u) {
+                    const float wu = __shfl_sync(0xffffffffu, w, c0 + u);
+                    if (wu != 0.f) {   // (0 for c0 + u >= G)
+#pragma unroll
+                        for (int k = 0; k < V; ++k) o[k] = fmaf(wu, v[u][k], o[k]);
+                    }
                 }
             }
-            float m = kLowest, L = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (lc[u] != 0.f) m = fmaxf(m, mc[u]);
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (lc[u] == 0.f) continue;   // no share of the row (and nothing written)
-                const float f = ex2f(mc[u] - m);
-                L = fmaf(f, lc[u], L);
-                o.x = fmaf(f, vc[u].x, o.x); o.y = fmaf(f, vc[u].y, o.y);
-                o.z = fmaf(f, vc[u].z, o.z); o.w = fmaf(f, vc[u].w, o.w);
-            }
-#pragma unroll
-            for (int k = 1; k <= 2; k <<= 1) {
-                L += __shfl_xor_sync(0xffffffffu, L, k);
-                o.x += __shfl_xor_sync(0xffffffffu, o.x, k);
-                o.y += __shfl_xor_sync(0xffffffffu, o.y, k);
-                o.z += __shfl_xor_sync(0xffffffffu, o.z, k);
-                o.w += __shfl_xor_sync(0xffffffffu, o.w, k);
-            }
-            if (cq == 0 && i < n) {
-                const float s = L == 0.f ? 0.f : rcp(L);
-                uint2 ob;
-                ob.x = pack_bf16(o.x * s, o.y * s);
-                ob.y = pack_bf16(o.z * s, o.w * s);
-                *reinterpret_cast<uint2 *>(A.out + ((int64_t)r * A.Hq + hb + h) * D + 4 * d4) = ob;
-                if (A.lse && d4 == 0)
-                    A.lse[(int64_t)r * A.Hq + hb + h] = L == 0.f ? -CUDART_INF_F : (m + log2f(L)) * 0.69314718055994531f;
-            }
+            uint32_t *out = reinterpret_cast<uint32_t *>(A.out + ((int64_t)r * A.Hq + h) * D) + lane * (V / 2);
+            if constexpr (V == 4) *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+            else *out = pack_bf16(o[0], o[1]);
+            if (A.lse && lane == 0) A.lse[(int64_t)r * A.Hq + h] = L == 0.f ? -CUDART_INF_F : (m + log2f(L)) * 0.69314718055994531f;
         }
         cluster_sync();   // nobody leaves while its parts are read
     }
