@@ -103,7 +103,7 @@ struct Cfg {
     static constexpr int kOffSc = kOffRows + 4 * kTile * 4;           // [2][3][128] score factor, log2 vs, 1 / vs
     static constexpr int kOffMax = kOffSc + 2 * 3 * kTile * 4;           // [4][HQP] maxima or sums of the quads
     static constexpr int kOffNegM = kOffMax + 4 * HQP * 4;            // [softmax warp][HG] minus the running maxima
-    static constexpr int kOffEpi = kOffNegM + 4 * HQP * 4;            // 1 / l, or a part's m and l [2][HQP]
+    static constexpr int kOffEpi = kOffNegM + 4 * HQP * 4;            // a part's m and l [HQP][2]
     static constexpr int kOffFlags = kOffEpi + 2 * HQP * 4;  // [group][4] heads to raise, by eights
     static constexpr int kOffMisc = kOffFlags + NG * 16;
     static constexpr int kUsed = kOffMisc + 64 + 16 * 8;
@@ -255,8 +255,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     extern __shared__ __align__(1024) uint8_t sm[];   // (no static shared memory: it begins 1024-byte aligned)
     int32_t *rows = reinterpret_cast<int32_t *>(sm + C::kOffRows);
     float *sc = reinterpret_cast<float *>(sm + C::kOffSc);
-    float *epi = reinterpret_cast<float *>(sm + C::kOffEpi);         // a row's 1 / l,
-    float2 *part_ml = reinterpret_cast<float2 *>(sm + C::kOffEpi);   // or its part's m and l
+    float2 *part_ml = reinterpret_cast<float2 *>(sm + C::kOffEpi);   // a part's m and l
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + C::kOffMisc);
     uint64_t *bar_s = bar, *bar_pv = bar + 2;   // S(t) done, one for each S buffer; P V(t) done
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 3);
@@ -820,9 +819,6 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 tc_fence_before();
                 if (__syncthreads_or(false)) break;   // a wait ran out
             }
-            bar_sync_n(kBarSoft, kSoft);   // P V of the last tile is done
-            tc_fence_after();
-
             // the row's sums over this warp's keys, each step on half as many heads as the
             // last: a lane ends with the sum of one head (HG = 16: of one half of the lanes)
             float v[HG];
@@ -844,18 +840,19 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             if (HG == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
             if (lane < HG) gmax[quad * HG + lane] = v[0];
             bar_sync_n(3 + 2 * hg, 128);
-            if (quad == 0 && lane < HG) {
+            if (lane < HG) {
                 const float L = (gmax[lane] + gmax[HG + lane]) + (gmax[2 * HG + lane] + gmax[3 * HG + lane]);
                 const int h = h0 + lane;
                 if (CL) {
-                    part_ml[h] = make_float2(m, L);
+                    if (quad == 0) part_ml[h] = make_float2(m, L);
                 } else {
-                    epi[h] = L == 0.f ? 0.f : rcp(L);
-                    if (A.lse && h < A.Hq)
+                    negm[lane] = L == 0.f ? 0.f : rcp(L);
+                    if (A.lse && quad == 0 && h < A.Hq)
                         A.lse[(int64_t)r * A.Hq + h] = L == 0.f ? -CUDART_INF_F : (m + log2f(L)) * 0.69314718055994531f;
                 }
             }
-            bar_sync_n(3 + 2 * hg, 128);
+            bar_sync_n(kBarSoft, kSoft);   // P V of the last tile is done
+            tc_fence_after();
             // O = O_hi + O_lo / 16: a part of a row as it is into shared memory (the K and V tiles
             // are idle by now), for the join; a row normalised and out, 64 bytes of a head a
             // store (staged for 16-byte stores: 2048 rows 85.5 us, so 82.3)
@@ -874,7 +871,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                         if (CL) {
                             part[(c + k) * D + key] = o;
                         } else {
-                            const __nv_bfloat16 ob = __float2bfloat16_rn(o * epi[h0 + c + k]);
+                            const __nv_bfloat16 ob = __float2bfloat16_rn(o * negm[c + k]);
                             if (h0 + c + k < A.Hq) out[(c + k) * D] = *reinterpret_cast<const uint16_t *>(&ob);
                         }
                     }
