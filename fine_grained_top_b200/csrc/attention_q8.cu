@@ -486,7 +486,9 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         float ks0 = 0.f, vs0 = 0.f;
         if (loader) {
             gather(i0, A.k, C::kOffK);
+            cp_async_commit();
             gather(i0, A.v, C::kOffV);
+            cp_async_commit();
             row0 = row_of(i0);
             if (row0 >= 0) {
                 ks0 = __ldg(A.k_scale + (row0 >> P.sb_shift));
@@ -522,7 +524,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             *reinterpret_cast<uint4 *>(sm + C::kOffQ + sw<D>(HQP + c / CPH, c % CPH)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         if (loader) put_scale(i0, row0, ks0, vs0);
-        cp_async_wait_all();
+        cp_async_wait<1>();   // the K tile; V's is waited for before P V
         fence_async_smem();
         __syncthreads();
 
