@@ -464,6 +464,81 @@ def test_attention_keeps_nan_to_the_rows_that_select_it(sa):
     assert torch.isnan(out[has]).all() and torch.isfinite(out[~has]).all()
 
 
+@pytest.mark.parametrize("Hq,T", [(5, 1), (64, 1), (33, 200)])
+def test_attention_keeps_odd_queries_to_their_heads(sa, Hq, T):
+    """Infinite and NaN queries make their own head's output NaN and no other; a row of zeros weighs its keys alike, and
+    the smallest numbers count."""
+    d, K, W, sb = 128, 96, 20, 64
+    x = attention_inputs([400], [T], T, Hq, d, K, W, sb, True, seed=20 + Hq)
+    x["q"][0, 1, 7], x["q"][0, 3, 100] = math.inf, math.nan
+    if T > 1:
+        x["q"][1] = 0
+        x["q"][2] = 2.0 ** -133   # bf16's smallest
+        x["q"][3, :, ::2] *= 2.0 ** -100
+        x["q"][4, 0] = -math.inf
+    got = run_attention(sa, x, T, Hq, d, K, W, sb)
+    assert got[2] == 0
+    odd = ~torch.isfinite(x["q"]).all(-1)
+    assert torch.isnan(got[0][odd]).all() and torch.isnan(got[1][odd]).all() and odd.sum() == 2 + (T > 1)
+    z = dict(x, q=torch.where(odd[..., None], torch.zeros_like(x["q"]), x["q"]))
+    plain = run_attention(sa, z, T, Hq, d, K, W, sb)
+    out, lse = got[0].clone(), got[1].clone()
+    out[odd], lse[odd] = plain[0][odd], plain[1][odd]
+    check_attention(z, (out, lse, 0), T, K, W, sb)
+
+
+def test_attention_of_many_rows_of_which_few_are_there(sa):
+    """200,000 rows, all but some of them padding."""
+    B, T, Hq, d, K, W, sb = 50, 4000, 3, 64, 12, 5, 16
+    g = torch.Generator().manual_seed(31)
+    lens = torch.randint(20, 90, (B,), generator=g).tolist()
+    x = attention_inputs(lens, [1 + b % 3 if b % 7 == 0 else 0 for b in range(B)], T, Hq, d, 0, W, sb, True, seed=31)
+    topk = torch.full((B * T, K), -1, dtype=torch.int32)
+    for r in torch.nonzero(x["nv"]).flatten().tolist():
+        topk[r, :6] = torch.randperm(int(x["nv"][r]), generator=g)[:6].sort().values.to(torch.int32)
+    x["topk"] = topk
+    out, lse, st = run_attention(sa, x, T, Hq, d, K, W, sb)
+    there = x["nv"] > 0
+    assert st == 0 and (out[~there] == 0).all() and (lse[~there] == -math.inf).all()
+    for b in range(0, B, 7):
+        rows = slice(b * T, b * T + 4)
+        want, wl, tol, tl, _ = ref.attention(x["q"][rows], x["kc"], x["vc"], x["ks"], x["vs"], sb, x["pt"][b:b + 1], x["S_max"],
+                                             x["nv"][rows], topk[rows], W, 4, d ** -0.5)
+        assert ((out[rows].double() - want).abs() <= tol).all()
+
+
+FIRST_CALL = """
+import sys, torch
+sys.path.insert(0, {root!r})
+import fine_grained_top_b200 as sa
+from tests import test_cache_ops_gpu as t
+for T, Hq in ((1, 64), (1, 16), (300, 32)):
+    x = t.attention_inputs([900] * 2, [T] * 2, T, Hq, 64, 256, 64, 64, True, seed=40)
+    y = {{n: v.cuda() for n, v in x.items() if isinstance(v, torch.Tensor)}}
+    out, lse = torch.zeros(2 * T, Hq, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(2 * T, Hq, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sa.sa_sparse_attn_q8(y["q"], y["kc"], y["vc"], y["ks"], y["vs"], 64, y["pt"], y["pt"].shape[1], x["pool"], 64, 0, y["nv"],
+                             y["topk"], 256, 64, 2, T, Hq, 64, 0.125, out, lse)
+    assert not out.any()
+    graph.replay()
+    torch.cuda.synchronize()
+    eager = t.run_attention(sa, x, T, Hq, 64, 256, 64, 64)
+    assert torch.equal(out.cpu(), eager[0]) and torch.equal(lse.cpu(), eager[1])
+print("same")
+"""
+
+
+def test_a_process_whose_first_calls_are_captured(sa):
+    import subprocess
+    import sys
+
+    from tests.conftest import ROOT
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL.format(root=str(ROOT))], capture_output=True, text=True, timeout=200)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
 @pytest.mark.parametrize("T", [1, 170])
 def test_attention_reports_bad_entries(sa, T):
     """A page id outside of the pool, a top-K entry behind the row's position, an unsorted row and a length beyond the
