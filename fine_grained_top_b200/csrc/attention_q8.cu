@@ -46,13 +46,20 @@
 // after another, spent its time on instruction-cache misses and single-warp
 // latencies: 288 us for those 2048 rows.)
 //
-// What bounds it.  Few rows: the chain row start -> lookups -> gather -> S -> P ->
-// P V -> join, 1.2 us a tile, and the launch: 8 rows of 2560 keys 13.2 us, 16 paged
-// ones 17.5.  Many rows: the softmax's issue slots (about half of them busy) behind
-// the latency of a tile's chain: 2048 rows of 1152 keys and 16 heads 89 us (6.8 TB/s
-// gathered, 212 TFLOP/s), 4 x 1024 rows of up to 2560 keys and 64 heads 367 us (421
-// TFLOP/s).  Two K and V tiles, S before P V and copies of the scales by cp.async
-// changed nothing or cost 2 percent.  Every wait is bounded (SA_DEV_TIMEOUT).
+// What bounds it.  Few rows: the launch and the chain row start -> lookups -> gather ->
+// S -> P -> P V -> join, of code that each CTA runs once (a row's start took 5800 cycles of
+// 19700 when a CTA had two tiles, the join 4200 before it went a head a warp): one row of
+// 1152 keys 6.7 us, 8 rows of 2560 keys and 64 heads 10.8, 16 such paged rows 15.1.  In the
+// loop a tile is 2100 cycles when a CTA has its SM alone (32 heads); in the 700 of them in
+// which its 12 MMAs run, by clock stamps, neither the lookups nor the scores' first read get
+// on.  Many rows: no unit is at its limit (issue slots 53 to 61 percent, tensor cores 11 to
+// 21, the gather 37 of its ceiling), it is that chain, two to four CTAs an SM deep.  2048
+// rows of 1152 keys and 16 heads 82 us (7.4 TB/s gathered, 232 TFLOP/s), 4 x 1024 padded rows
+// of up to 2560 keys and 64 heads 355 us (436 TFLOP/s), of which raises take 44: a group of
+// 32 heads has one in a third of its tiles.  Two K and V tiles, S before P V, copies of the scales by cp.async, Q's parts
+// side by side for 32 heads (half of S's operand reads, but two CTAs an SM instead of three),
+// and raises that sweep up the heads next in line changed nothing or cost 1 to 10 percent.
+// Every wait is bounded (SA_DEV_TIMEOUT).
 #include <math_constants.h>
 
 #include <algorithm>
