@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         // Only the MMA warp polls: warps that poll take issue slots from those that compute,
         // and warps that wait at a barrier do not.  It tells the loader warps when P V(t - 1) and
         // S(t + 1) are done, and the softmax warps when P V(t - 1) is.
-        constexpr int kBarSoft = 6, kSoft = C::kThreads - 128, kBarV = 1, kBarK = 7, kLoad = 160;
+        constexpr int kBarSoft = 6, kBarVote = 8, kSoft = C::kThreads - 128, kBarV = 1, kBarK = 7, kLoad = 160;
         if (warp == C::kWarpMma) {
             // ------------------------------------------------------------ MMA warp
             if (elect_one()) issue_s(i0);
@@ -589,13 +589,18 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 if (elect_one()) {
                     tc_fence_after();
                     issue_pv(t);
-                    if (t + 2 < i1) issue_s(t + 2);
                 }
                 __syncwarp();
                 ok = wait_pv(t);
                 bar_arrive_n(kBarSoft, kSoft);
                 if (t + 1 < i1) bar_arrive_n(kBarV, kLoad);
                 if (t + 2 < i1) {
+                    // Not before the vote on tile t + 1 has read its scores: reads that meet MMAs
+                    // wait.  (4 x 1024 rows of 64 heads 326 us; behind P V's end 348, right behind
+                    // P V in one go 355.)
+                    bar_sync_n(kBarVote, kSoft);
+                    if (ok && elect_one()) issue_s(t + 2);
+                    __syncwarp();
                     ok = ok && wait_s(t + 2);
                     bar_arrive_n(kBarK, kLoad);
                 }
@@ -732,6 +737,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                         top = max3(top, f.x, f.y);
                     }
                 }
+                if (t > i0 && t + 1 < i1) bar_arrive_n(kBarVote, kSoft);
                 const bool raise = bar_or(2 + 2 * hg, 128, top > kRaise);
                 if (t > i0) bar_sync_n(kBarSoft, kSoft);   // P V(t - 1) is done: O is whole, the P tile is free
                 tc_fence_after();
