@@ -35,7 +35,7 @@
 //                    into the single P tile.  32 heads keep their sums in registers
 //                    and read the scores from TMEM twice; 64 a thread spill, and 16
 //                    with four groups read each key's factors twice as often
-//   1 MMA warp       issues P V(t) and S(t+2) (two S buffers), is the only one that
+//   1 MMA warp       issues P V(t), then S(t+2) (two S buffers), is the only one that
 //                    polls their mbarriers, and passes each end on over a named
 //                    barrier: polling warps took issue slots from the softmax
 //                    (32 x 4 rows: 24.2 us with the loaders polling, 21.7 so)
@@ -49,17 +49,18 @@
 // What bounds it.  Few rows: the launch and the chain row start -> lookups -> gather ->
 // S -> P -> P V -> join, of code that each CTA runs once (a row's start took 5800 cycles of
 // 19700 when a CTA had two tiles, the join 4200 before it went a head a warp): one row of
-// 1152 keys 6.7 us, 8 rows of 2560 keys and 64 heads 10.8, 16 such paged rows 15.1.  In the
-// loop a tile is 2100 cycles when a CTA has its SM alone (32 heads); in the 700 of them in
-// which its 12 MMAs run, by clock stamps, neither the lookups nor the scores' first read get
-// on.  Many rows: no unit is at its limit (issue slots 53 to 61 percent, tensor cores 11 to
-// 21, the gather 37 of its ceiling), it is that chain, two to four CTAs an SM deep.  2048
-// rows of 1152 keys and 16 heads 82 us (7.4 TB/s gathered, 232 TFLOP/s), 4 x 1024 padded rows
-// of up to 2560 keys and 64 heads 355 us (436 TFLOP/s), of which raises take 44: a group of
-// 32 heads has one in a third of its tiles.  Two K and V tiles, S before P V, copies of the scales by cp.async, Q's parts
-// side by side for 32 heads (half of S's operand reads, but two CTAs an SM instead of three),
-// and raises that sweep up the heads next in line changed nothing or cost 1 to 10 percent.
-// Every wait is bounded (SA_DEV_TIMEOUT).
+// 1152 keys 6.6 us, 8 rows of 2560 keys and 64 heads 10.8, 16 such paged rows 14.7.  In the
+// loop a tile is about 2000 cycles when a CTA has its SM alone (32 heads); while its MMAs
+// run, by clock stamps, neither the lookups nor reads of the scores get on, hence the order
+// in the MMA warp.  Many rows: no unit is at its limit (issue slots and tensor pipe about 60
+// and 20 percent, the gather 40 of its ceiling), it is that chain, two to four CTAs an SM
+// deep.  2048 rows of 1152 keys and 16 heads 78 us (7.7 TB/s gathered, 243 TFLOP/s), 4 x
+// 1024 padded rows of up to 2560 keys and 64 heads 327 us (473 TFLOP/s), of which raises
+// take 40: a group of 32 heads has one in a third of its tiles.  Two K and V tiles, S before
+// P V, P V or the vote elsewhere in the tile, copies of the scales by cp.async, Q's parts side
+// by side for 32 heads (half of S's operand reads, but two CTAs an SM instead of three), and
+// raises that sweep up the heads next in line changed nothing or cost 1 to 25 percent.  Every
+// wait is bounded (SA_DEV_TIMEOUT).
 #include <math_constants.h>
 
 #include <algorithm>
