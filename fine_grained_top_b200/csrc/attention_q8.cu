@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     // wait.  (4 x 1024 rows of 64 heads 326 us; behind P V's end 348, right behind
                     // P V in one go 355.)
                     bar_sync_n(kBarVote, kSoft);
-                    if (ok && elect_one()) issue_s(t + 2);
+                    if (elect_one() && ok) issue_s(t + 2);
                     __syncwarp();
                     ok = ok && wait_s(t + 2);
                     bar_arrive_n(kBarK, kLoad);
