@@ -66,8 +66,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include "gather_pipe.cuh"
-#include "internal.h"
+#include "cache_ops.h"
 #include "ptx.cuh"
 
 namespace sa {
@@ -156,6 +155,43 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     f2 r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// Arrive at barrier `id` of `n` threads without waiting for it; wait for it; wait and return the OR of a predicate.
+__device__ __forceinline__ void bar_arrive_n(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ void bar_sync_n(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ bool bar_or(int id, int n, bool p) {
+    uint32_t r;
+    asm volatile(
+        "{ .reg .pred a, b; setp.ne.u32 a, %1, 0; bar.red.or.pred b, %2, %3, a; selp.u32 %0, 1, 0, b; }"
+        : "=r"(r)
+        : "r"((uint32_t)p), "r"(id), "r"(n)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ float ex2f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait_all() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// MN-major operand without swizzle: 8 x 16-byte core matrices (8 K rows of 8
+// MN elements, 128 contiguous bytes); K groups of 8 rows `kgroup` bytes apart,
+// MN chunks of 8 elements `mnchunk` bytes apart.  (For this layout the
+// descriptor's leading offset is the K-group stride and its stride offset the
+// MN-chunk stride.)
+__device__ __forceinline__ uint64_t desc_mn_plain(uint32_t addr, uint32_t kgroup, uint32_t mnchunk) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3FFF);
+    d |= (uint64_t)((kgroup >> 4) & 0x3FFF) << 16;
+    d |= (uint64_t)((mnchunk >> 4) & 0x3FFF) << 32;
+    d |= (uint64_t)1 << 46;   // layout type 0 (no swizzle) in bits 61-63
+    return d;
 }
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }

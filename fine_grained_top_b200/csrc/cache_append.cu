@@ -26,7 +26,7 @@
 //          from the registers once the scales are known.
 #include <algorithm>
 
-#include "internal.h"
+#include "cache_ops.h"
 #include "ptx.cuh"
 
 namespace sa {

@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "../../include/sa.h"
+#include "cache_ops.h"
 #include "internal.h"
 
 using namespace sa;
