@@ -26,7 +26,7 @@
 // a row's tiles: a thread-block cluster shares the row, and the partial m, l, O
 // meet through distributed shared memory.  A tile is 128 keys.  The warps:
 //   4 loader warps   one key a thread looked up ahead (selection entry four tiles
-//                    ahead, page three, scales one), V(t) and K(t+2) copied with
+//                    ahead, page three, scales two), V(t) and K(t+2) copied with
 //                    16-byte cp.async as soon as P V(t-1) and S(t+1) let go of the
 //                    single V and K tiles (a slot without a key is zero-filled:
 //                    nothing that was not selected is ever read)
@@ -490,8 +490,8 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             }
             // in the order the copies take them: key RPT i + c is number i of the c-th row of threads
             rows[(t & 3) * kTile + (tid % RPT) * NIT + tid / RPT] = row;
+            return row;
         };
-        auto row_of = [&](int t) { return rows[(t & 3) * kTile + (tid % RPT) * NIT + tid / RPT]; };
         auto put_scale = [&](int t, int row, float ks, float vs) {
             vs = clamp_scale(vs);
             float *o = sc + (t & 1) * 3 * kTile + tid;
@@ -500,6 +500,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             o[2 * kTile] = row >= 0 ? rcp(vs) : 0.f;
         };
         int pos3 = -1;   // the position of tile t + 3's key
+        int row[NP] = {-1, -1, -1};   // the rows of tiles t, t + 1 and t + 2's (the loaders' own: reads that meet MMAs wait)
         if (loader) {
             if (n_top != A.K || i0 != g0) {   // it came otherwise
 #pragma unroll
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             pos3 = position(i0 + 3);
 #pragma unroll
             for (int t = 0; t < NP; ++t)
-                put_row(i0 + t, i0 + t < i1 && (i0 + t) * kTile + tid < n_keys ? pos_g[t] : -1, page_g[t]);
+                row[t] = put_row(i0 + t, i0 + t < i1 && (i0 + t) * kTile + tid < n_keys ? pos_g[t] : -1, page_g[t]);
         }
         __syncthreads();
 
@@ -526,17 +527,15 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             for (int i = 0; i < NIT; ++i)
                 cp_async16_or_zero(to + i * RPT * D, from + (int64_t)max(ids[i], 0) * D, ids[i] >= 0);
         };
-        int row0 = -1;
         float ks0 = 0.f, vs0 = 0.f;
         if (loader) {
             gather(i0, A.k, C::kOffK);
             cp_async_commit();
             gather(i0, A.v, C::kOffV);
             cp_async_commit();
-            row0 = row_of(i0);
-            if (row0 >= 0) {
-                ks0 = __ldg(A.k_scale + (row0 >> P.sb_shift));
-                vs0 = __ldg(A.v_scale + (row0 >> P.sb_shift));
+            if (row[0] >= 0) {
+                ks0 = __ldg(A.k_scale + (row[0] >> P.sb_shift));
+                vs0 = __ldg(A.v_scale + (row[0] >> P.sb_shift));
             }
         }
         // both parts of this thread's chunks of Q, while the copies fly (heads >= Hq are zeros)
@@ -567,7 +566,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             *reinterpret_cast<uint4 *>(sm + C::kOffQ + sw<D>(c / CPH, c % CPH)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4 *>(sm + C::kOffQ + sw<D>(HQP + c / CPH, c % CPH)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
-        if (loader) put_scale(i0, row0, ks0, vs0);
+        if (loader) put_scale(i0, row[0], ks0, vs0);
         cp_async_wait<1>();   // the K tile; V's is waited for before P V
         fence_async_smem();
         __syncthreads();
@@ -646,6 +645,10 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         } else if (loader) {
             // ------------------------------------------------------------ loader warps
             regs_dec<C::kRegsLoad>();
+            if (row[1] >= 0) {
+                ks0 = __ldg(A.k_scale + (row[1] >> P.sb_shift));
+                vs0 = __ldg(A.v_scale + (row[1] >> P.sb_shift));
+            }
             if (i0 + 1 < i1) {
                 bar_sync_n(kBarK, kLoad);   // S(i0) is done: the K tile is free
                 gather(i0 + 1, A.k, C::kOffK);
@@ -654,12 +657,12 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 bar_arrive_n(kBarV, kLoad);
             }
             for (int t = i0; t < i1; ++t) {
-                // lookups ahead: the page of tile t + 3's key, the scales of tile t + 1's
-                const int pg3 = page_of(pos3), row1 = row_of(t + 1);
-                float ks1 = 0.f, vs1 = 0.f;
-                if (t + 1 < i1 && row1 >= 0) {
-                    ks1 = __ldg(A.k_scale + (row1 >> P.sb_shift));
-                    vs1 = __ldg(A.v_scale + (row1 >> P.sb_shift));
+                // lookups ahead: the page of tile t + 3's key, the scales of tile t + 2's
+                const int pg3 = page_of(pos3);
+                const float ks1 = ks0, vs1 = vs0;
+                if (row[2] >= 0) {
+                    ks0 = __ldg(A.k_scale + (row[2] >> P.sb_shift));
+                    vs0 = __ldg(A.v_scale + (row[2] >> P.sb_shift));
                 }
                 const int pos4 = position(t + 4);
                 if (t > i0) {
@@ -669,9 +672,10 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 if (t + 1 < i1) {
                     bar_sync_n(kBarK, kLoad);   // S(t + 1) is done: K(t + 2) over K(t + 1)
                     if (t + 2 < i1) gather(t + 2, A.k, C::kOffK);
-                    put_scale(t + 1, row1, ks1, vs1);
+                    put_scale(t + 1, row[1], ks1, vs1);
                 }
-                put_row(t + 3, pos3, pg3);
+                row[1] = row[2];
+                row[2] = put_row(t + 3, pos3, pg3);
                 pos3 = pos4;
                 cp_async_wait_all();
                 fence_async_smem();
