@@ -49,13 +49,13 @@
 // What bounds it.  Few rows: the launch and the chain row start -> lookups -> gather ->
 // S -> P -> P V -> join, of code that each CTA runs once (a row's start took 5800 cycles of
 // 19700 when a CTA had two tiles, the join 4200 before it went a head a warp): one row of
-// 1152 keys 6.6 us, 8 rows of 2560 keys and 64 heads 10.8, 16 such paged rows 14.7.  In the
-// loop a tile is about 2000 cycles when a CTA has its SM alone (32 heads); while its MMAs
+// 1152 keys 6.6 us, 8 rows of 2560 keys and 64 heads 10.8, 16 such paged rows 14.6.  In the
+// loop a tile is 1600 to 1900 cycles when a CTA has its SM alone (32 heads); while its MMAs
 // run, by clock stamps, neither the lookups nor reads of the scores get on, hence the order
 // in the MMA warp.  Many rows: no unit is at its limit (issue slots and tensor pipe about 60
 // and 20 percent, the gather 40 of its ceiling), it is that chain, two to four CTAs an SM
-// deep.  2048 rows of 1152 keys and 16 heads 78 us (7.7 TB/s gathered, 243 TFLOP/s), 4 x
-// 1024 padded rows of up to 2560 keys and 64 heads 327 us (473 TFLOP/s), of which raises
+// deep.  2048 rows of 1152 keys and 16 heads 76 us (7.9 TB/s gathered, 249 TFLOP/s), 4 x
+// 1024 padded rows of up to 2560 keys and 64 heads 324 us (477 TFLOP/s), of which raises
 // take 40: a group of 32 heads has one in a third of its tiles.  Two K and V tiles, S before
 // P V, P V or the vote elsewhere in the tile, copies of the scales by cp.async, Q's parts side
 // by side for 32 heads (half of S's operand reads, but two CTAs an SM instead of three), and
