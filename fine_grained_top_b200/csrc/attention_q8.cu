@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     __syncwarp();
                 }
                 // One vote of the group a tile: does any head need a new reference?
-                // (KEEP: the first 16 heads' e is kept for P.  2048 rows of 36 tiles: 92 us
+                // (KEEP: the first 16 heads' e is kept for P.  2048 rows of 9 tiles: 92 us
                 // without, 88 with; the cluster form would spill.)
                 constexpr bool KEEP = !CL;
                 f2 e0[8];
