@@ -5,31 +5,36 @@
 //   S(r) = {s in TopK(r) : s <= p - W}  U  {max(0, p-W+1) .. p}
 //   x_s = (q[r,h] . kc[s]) ks[s] scale,   O[r,h] = sum_s softmax(x)_s vs[s] vc[s]
 //
-// The codes go into the tensor cores as they lie in the cache (tcgen05
-// kind::f8f6f4, e4m3 x e4m3 products are exact, fp32 sums): nothing is
-// widened on the way, so a key costs 2 d bytes of gather and no conversions.
-// The 16-bit operands are split instead, into two e4m3 parts side by side on
-// the MMA's N dimension: q 2^-e = q_hi + q_lo (exact for a bf16 q down to 2^-10
-// of the row's largest value, below it off by 2^-18 of that), P = P_hi + P_lo / 16
-// (off by 2^-8 of its value, 2^-14 among the smallest).  The scales stay out of
-// the products: in
-//   S^T = K Q^T        M = 128 keys, N = 2 x heads, K = d            -> TMEM
+// Two products on the tensor cores, each with fp32 sums:
+//   S^T = K Q^T        M = 128 keys, N = heads, K = d            -> TMEM
 //   P^T                softmax over keys, one thread per key lane
-//   O^T += V^T P^T     M = d, N = 2 x heads, K = 128 keys            -> TMEM
-// a key is a lane, so ks and vs are one number per thread: with
+//   O^T += V^T P^T     M = d, N = heads, K = 128 keys            -> TMEM
+// S takes the codes as they lie in the cache (tcgen05 kind::f8f6f4, e4m3 x e4m3
+// products are exact) and q split into two e4m3 parts: q 2^-e = q_hi + q_lo (exact for
+// a bf16 q down to 2^-10 of the row's largest value, below it off by 2^-18 of that).
+// P V is a product of fp16 (kind::f16): V's codes are widened on the way (exactly), and
+// P is rounded once.  P has to keep its precision over many orders of magnitude: a key
+// that takes most of the weight with next to no value of its own (an attention sink)
+// leaves the output to keys 2^-10 to 2^-20 of it.  (Two e4m3 parts of P, which let V go in
+// as it is, end at 2^-14: such a head's output was off by up to its whole size.)
+// The scales stay out of the products: in S^T a key is a lane, so ks and vs are one
+// number per thread: with
 //   e = (S_hi + S_lo) ks 2^e scale log2e + log2 vs - m,    P = 2^e
-// the running maximum m is of the contributions p vs (so P fills e4m3's range
-// whatever the scales), and the row sum takes P / vs.  After a raise of m the
-// largest P is 2; it may grow to 2^8.75 (e4m3 ends at 448) before the next.
+// the running maximum m is of the contributions p vs (so P fills fp16's range whatever
+// the scales), and the row sum takes P / vs.  P's largest is 2^8 after the first tile; it
+// may grow to 2^15.75 (fp16 ends at 2^16) before m goes up, by 2^8: so a head's largest is
+// always at least 2^7.75, and a P is off by 2^-11 of its value and, where fp16 runs out of
+// exponents, by 2^-25, which is 2^-32 of that largest.
 //
 // A CTA takes one row, or (few rows: the cost rule in launch_q8_rows) one run of
 // a row's tiles: a thread-block cluster shares the row, and the partial m, l, O
 // meet through distributed shared memory.  A tile is 128 keys.  The warps:
 //   4 loader warps   one key a thread looked up ahead (selection entry four tiles
-//                    ahead, page three, scales two), V(t) and K(t+2) copied with
-//                    16-byte cp.async as soon as P V(t-1) and S(t+1) let go of the
-//                    single V and K tiles (a slot without a key is zero-filled:
-//                    nothing that was not selected is ever read)
+//                    ahead, page three, scales two).  V's codes are loaded into registers a
+//                    tile ahead and widened into the V tile as soon as P V(t-1) lets go of
+//                    it; K(t+2) is copied with 16-byte cp.async as soon as S(t+1) lets go of
+//                    the single K tile (a slot without a key is zero-filled: nothing that
+//                    was not selected is ever read).  Both fly while P V(t) runs
 //   4 or 8 softmax   one key a lane, 16 heads a thread with up to 16 heads, else 32
 //     warps          (two groups with 64): a vote on raises, the exponentials, P^T
 //                    into the single P tile.  32 heads keep their sums in registers
@@ -37,30 +42,22 @@
 //                    with four groups read each key's factors twice as often
 //   1 MMA warp       issues P V(t), then S(t+2) (two S buffers), is the only one that
 //                    polls their mbarriers, and passes each end on over a named
-//                    barrier: polling warps took issue slots from the softmax
-//                    (32 x 4 rows: 24.2 us with the loaders polling, 21.7 so)
+//                    barrier: polling warps take issue slots from the softmax
 // and one barrier of the CTA a tile hands P(t), V(t) and the next factors over.
-// The loaders give registers to the softmax warps (setmaxnreg; without it 2048
-// rows take 119 us instead of 99), so that two (64 heads) to four CTAs share an SM and
-// fill each other's waits.  (A persistent CTA of 16 to 24 warps in roles, a row
-// after another, spent its time on instruction-cache misses and single-warp
-// latencies: 288 us for those 2048 rows.)
+// Two (from 17 heads) or three CTAs share an SM and fill each other's waits.  (A
+// persistent CTA of 16 to 24 warps in roles, a row after another, spent its time on
+// instruction-cache misses and single-warp latencies: three times as long for 2048 rows.)
 //
 // What bounds it.  Few rows: the launch and the chain row start -> lookups -> gather ->
-// S -> P -> P V -> join, of code that each CTA runs once (a row's start took 5800 cycles of
-// 19700 when a CTA had two tiles, the join 4200 before it went a head a warp): one row of
-// 1152 keys 6.6 us, 8 rows of 2560 keys and 64 heads 10.8, 16 such paged rows 14.6.  In the
-// loop a tile is 1600 to 1900 cycles when a CTA has its SM alone (32 heads); while its MMAs
-// run, by clock stamps, neither the lookups nor reads of the scores get on, hence the order
-// in the MMA warp.  Many rows: no unit is at its limit (issue slots and tensor pipe about 60
-// and 20 percent, the gather 40 of its ceiling), it is that chain, two to four CTAs an SM
-// deep.  2048 rows of 1152 keys and 16 heads 76 us (7.9 TB/s gathered, 249 TFLOP/s), 4 x
-// 1024 padded rows of up to 2560 keys and 64 heads 324 us (477 TFLOP/s), of which raises
-// take 40: a group of 32 heads has one in a third of its tiles.  Two K and V tiles, S before
-// P V, P V or the vote elsewhere in the tile, copies of the scales by cp.async, Q's parts side
-// by side for 32 heads (half of S's operand reads, but two CTAs an SM instead of three), and
-// raises that sweep up the heads next in line changed nothing or cost 1 to 25 percent.  Every
-// wait is bounded (SA_DEV_TIMEOUT).
+// S -> P -> P V -> join, of code that each CTA runs once: one row of 1152 keys 6.4 us, 8
+// rows of 2560 keys and 64 heads 10.5, 16 such paged rows 14.4.  While a CTA's MMAs run
+// neither the lookups nor reads of the scores get on, hence the order in the MMA warp.
+// Many rows: that same chain, two or three CTAs an SM deep, as many as V in fp16 leaves
+// room for.  2048 rows of 1152 keys and 16 heads 100 us (issue slots 56 percent, shared
+// memory 68), 4 x 1024 padded rows of up to 2560 keys and 64 heads 377 us (410 TFLOP/s).
+// V's codes in registers instead of a stage of their own in shared memory: 106 and 379;
+// both copies before the barrier of the tile: 107 and 393.  Every wait is bounded
+// (SA_DEV_TIMEOUT).
 #include <math_constants.h>
 
 #include <algorithm>
@@ -74,7 +71,7 @@ namespace sa {
 namespace {
 
 constexpr int kTile = 128;                  // keys per tile (MMA M)
-constexpr float kTop = 1.f, kRaise = 8.75f; // log2 of a row's largest P at first, and of what it may grow to
+constexpr float kTop = 8.f, kRaise = 15.75f; // log2 of a row's largest P at first, and of what it may grow to
 constexpr float kStep = 8.f;                // how far a head's reference goes up then
 constexpr float kLowest = -3.4028235e38f;   // running maximum of a head that has met no finite score yet
 constexpr float kCoarse = 8388608.f;        // a reference from 2^23 on is not moved by steps
@@ -97,36 +94,31 @@ struct Cfg {
     static constexpr int NG = HQP / HG;                   // softmax groups of 128 threads
     static constexpr int kThreads = 128 + 128 * NG + 32;  // loader warps, softmax warps, the MMA warp
     static constexpr int kWarpMma = 4 + 4 * NG;
-    static constexpr int kKV = kTile * D, kQ = N2 * D, kP = kTile * N2;
+    static constexpr int kKV = kTile * D, kQ = N2 * D, kP = kTile * HQP * 2;
     static constexpr int kOffK = 0;
     // Q's parts: one after the other into the same columns of S, or with 16 heads side
     // by side (half the MMAs, which are all of the least size, for one more addition)
     static constexpr bool kSide = HQP == 16;
     static constexpr int SN = kSide ? N2 : HQP;           // columns of an S buffer
-    static constexpr int kOffV = kOffK + kKV;
-    static constexpr int kOffQ = kOffV + kKV;
+    static constexpr int kOffV = kOffK + kKV;            // V in fp16: halves of 64 dims, 128 bytes a key
+    static constexpr int kOffQ = kOffV + 2 * kKV;
     static constexpr int kOffP = kOffQ + kQ;
-    static constexpr int kOffRows = kOffP + kP;                   // [4][128] cache rows of a tile's keys
-    static constexpr int kOffSc = kOffRows + 4 * kTile * 4;           // [2][3][128] score factor, log2 vs, 1 / vs
-    static constexpr int kOffMax = kOffSc + 2 * 3 * kTile * 4;           // [4][HQP] maxima or sums of the quads
+    static constexpr int kOffSc = kOffP + kP;                         // [2][2][128] score factor, log2 vs
+    static constexpr int kOffMax = kOffSc + 2 * 2 * kTile * 4;           // [4][HQP] maxima or sums of the quads
     static constexpr int kOffNegM = kOffMax + 4 * HQP * 4;            // [softmax warp][HG] minus the running maxima
     static constexpr int kOffEpi = kOffNegM + 4 * HQP * 4;            // a part's m and l [HQP][2]
     static constexpr int kOffFlags = kOffEpi + 2 * HQP * 4;  // [group][4] heads to raise, by eights
     static constexpr int kOffMisc = kOffFlags + NG * 16;
     static constexpr int kUsed = kOffMisc + 64 + 16 * 8;
-    static constexpr uint32_t kTmemCols = 2 * SN + N2 <= 64 ? 64 : (2 * SN + N2 <= 128 ? 128 : 256);   // two S buffers, O
+    static constexpr uint32_t kTmemCols = 2 * SN + HQP <= 64 ? 64 : (2 * SN + HQP <= 128 ? 128 : 256);   // two S buffers, O
     // CTAs wait for TMEM columns while others of their cluster wait for them, so
     // whatever shares an SM must fit its 512 columns: shared memory in proportion.
     static constexpr int kLeast = (int)(kTmemCols * (kSmemSm / 512)) - 1024;
     static constexpr int kSmem = kUsed > kLeast ? kUsed : kLeast;
-    // CTAs an SM: two to four by their registers.  The loader warps hand most of
-    // theirs to the softmax warps.
-    static constexpr int kByRegs = HQP == 16 ? 4 : (HQP == 32 ? 3 : 2);
-    static constexpr int kRegs = HQP == 16 ? 56 : 72, kRegsLoad = 40, kRegsSoft = HQP == 16 ? 72 : (HQP == 32 ? 104 : 88);
-    static_assert(kRegsLoad * 128 + kRegsSoft * 128 * NG + kRegs * 32 <= kRegs * kThreads, "registers of the launch");
-    static_assert(kRegs * kThreads * kByRegs <= 65536, "registers of an SM");
-    static constexpr int kPerSm = kSmemSm / (kSmem + 1024) < kByRegs ? kSmemSm / (kSmem + 1024) : kByRegs;
-    static_assert(2 * kKV >= HQP * D * 4, "O lies in the K and V tiles when a row or its part is done");
+    // CTAs an SM, by their shared memory and registers (with 64 dims and 16 heads a fourth
+    // would fit, and spill: 2048 rows 80 us with three, 93 with four)
+    static constexpr int kPerSm = std::min(kSmemSm / (kSmem + 1024), HQP == 16 ? 3 : 2);
+    static_assert(3 * kKV >= HQP * D * 4, "O lies in the K and V tiles when a row or its part is done");
 };
 
 // ------------------------------------------------------------------ helpers
@@ -193,10 +185,6 @@ __device__ __forceinline__ uint64_t desc_mn_plain(uint32_t addr, uint32_t kgroup
     d |= (uint64_t)1 << 46;   // layout type 0 (no swizzle) in bits 61-63
     return d;
 }
-template <int N>
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[8]) { tmem_ld_x8(taddr, r); }
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_x16(taddr, r); }
 __device__ __forceinline__ bool elect_one() {
@@ -243,11 +231,6 @@ __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 __device__ __forceinline__ float clamp_scale(float s) {   // into [2^-64, 2^64]; NaN -> 2^-64
     return fminf(fmaxf(s, 5.421010862427522e-20f), 1.8446744073709552e19f);
 }
@@ -277,17 +260,28 @@ template <int D>
 __device__ __forceinline__ uint32_t sw(int r, int ch) {
     return (uint32_t)(r * D + ((D == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3)) << 4));
 }
-// MN-major operand of D-byte K rows with the D-byte swizzle.  D = 64: the MMA's
-// upper 64 M rows read the same 64 dims again (a stride of 0 between the MN
-// chunks); their results are not used.
+// Byte offset of 16-byte chunk `ch` (8 dims) of key `r` in the fp16 V tile: 128-byte
+// swizzled rows of 64 dims, two halves of them with 128 dims.
+__device__ __forceinline__ uint32_t sw_v(int r, int ch) {
+    return (uint32_t)((ch >> 3) * (kTile * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+}
+// The MN-major operand of that tile: 8-row K groups 1024 bytes apart.  D = 64: the MMA's
+// upper 64 M rows read the same 64 dims again (a stride of 0 between the MN chunks);
+// their results are not used.
 template <int D>
 __device__ __forceinline__ uint64_t desc_v(uint32_t addr) {
     uint64_t d = 0;
     d |= (uint64_t)((addr >> 4) & 0x3FFF);
-    d |= (uint64_t)((8 * D) >> 4) << 32;      // 8-row K groups
+    d |= (uint64_t)(((D == 128 ? kTile * 128 : 0) >> 4) & 0x3FFF) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
     d |= (uint64_t)1 << 46;
-    d |= (uint64_t)(D == 128 ? 2 : 4) << 61;
+    d |= (uint64_t)2 << 61;   // 128-byte swizzle
     return d;
+}
+// Instruction descriptor, kind::f16 with both operands fp16 (format code 0), f32
+// accumulate, both MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16_mn(int M, int N) {
+    return (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // CL: a cluster shares the row (the two forms are apart to keep the code, and the
@@ -295,9 +289,8 @@ __device__ __forceinline__ uint64_t desc_v(uint32_t addr) {
 template <int D, int HQP, bool CL>
 __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) attn_q8_kernel(Params P) {
     using C = Cfg<D, HQP>;
-    constexpr int N2 = C::N2, NT = C::kThreads, HG = C::HG, SN = C::SN;
+    constexpr int NT = C::kThreads, HG = C::HG, SN = C::SN;
     extern __shared__ __align__(1024) uint8_t sm[];   // (no static shared memory: it begins 1024-byte aligned)
-    int32_t *rows = reinterpret_cast<int32_t *>(sm + C::kOffRows);
     float *sc = reinterpret_cast<float *>(sm + C::kOffSc);
     float2 *part_ml = reinterpret_cast<float2 *>(sm + C::kOffEpi);   // a part's m and l
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + C::kOffMisc);
@@ -317,9 +310,8 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     // the start of its top-K row (16 bytes a thread and turn), and the selection's entries
     // of this CTA's first three tiles if the top-K row is full, as most are.  The pages of
     // those follow as soon as the length is there.  (Each after the barrier that makes it
-    // certain: 32 x 4 rows 21.9 us instead of 21.0, 3 x 37 small ones 6.4 instead of 6.0.
-    // The second turn over the top-K row pays with the longer rows that go with 64 heads:
-    // 8 rows of 2560 keys 13.4 us without it, 13.0 with; 2048 rows of 16 heads 88 and 91.)
+    // certain costs 4 percent.  The second turn over the top-K row pays with the longer rows
+    // that go with 64 heads.)
     const int nv = __ldg(A.n_valid + r);
     const int32_t *trow = A.topk + (int64_t)r * A.K;
     const int32_t *pt = A.page_table ? A.page_table + (int64_t)b * A.max_pages : nullptr;
@@ -452,7 +444,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);   // two S buffers (SN columns each), O (N2 columns)
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);   // two S buffers (SN columns each), O (HQP columns)
     const uint2 part = found[min(lane, NT / 32 - 1)];
     const int n_top = p >= 0 ? (int)__reduce_min_sync(0xffffffffu, part.x) : 0;
     const uint32_t q_max = __reduce_max_sync(0xffffffffu, part.y & 0xFFFFu), q_odd = __any_sync(0xffffffffu, part.y >> 16);
@@ -474,33 +466,28 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         const float down = __int_as_float((127 - e2) << 23);
         const float factor = __int_as_float((e2 + 127) << 23) * P.scale_log2;
 
-        constexpr int RPT = 128 / CPH, NIT = kTile / RPT;   // rows that the loader threads copy at once, turns
+        constexpr int RPT = 32 / CPH, NIT = 32 / RPT;   // rows that a loader warp copies at once, turns for its 32
         // lookups of the loader threads, one key each: position (-1: none), page, cache row, scales
         auto position = [&](int t) {
             const int kk = t * kTile + tid;
             return t < i1 && kk < n_keys ? (kk < n_top ? __ldg(trow + kk) : w0 + (kk - n_top)) : -1;
         };
         auto page_of = [&](int pos) { return pos >= 0 && pt ? __ldg(pt + (pos >> 6)) : 0; };
-        auto put_row = [&](int t, int pos, int page) {
-            int row = -1;
-            if (pos >= 0) {
-                if (!pt) row = b * A.S_max + pos;
-                else if (page >= 0 && page < A.pool_pages) row = page * 64 + (pos & 63);
-                else report(A.dev_status, SA_DEV_INDEX);
-            }
-            // in the order the copies take them: key RPT i + c is number i of the c-th row of threads
-            rows[(t & 3) * kTile + (tid % RPT) * NIT + tid / RPT] = row;
-            return row;
+        auto row_of = [&](int pos, int page) {
+            if (pos < 0) return -1;
+            if (!pt) return b * A.S_max + pos;
+            if (page >= 0 && page < A.pool_pages) return page * 64 + (pos & 63);
+            report(A.dev_status, SA_DEV_INDEX);
+            return -1;
         };
         auto put_scale = [&](int t, int row, float ks, float vs) {
             vs = clamp_scale(vs);
-            float *o = sc + (t & 1) * 3 * kTile + tid;
+            float *o = sc + (t & 1) * 2 * kTile + tid;
             o[0] = row >= 0 ? clamp_scale(ks) * factor : 0.f;
             o[kTile] = row >= 0 ? __log2f(vs) : -CUDART_INF_F;
-            o[2 * kTile] = row >= 0 ? rcp(vs) : 0.f;
         };
         int pos3 = -1;   // the position of tile t + 3's key
-        int row[NP] = {-1, -1, -1};   // the rows of tiles t, t + 1 and t + 2's (the loaders' own: reads that meet MMAs wait)
+        int row[NP] = {-1, -1, -1};   // the cache rows of tiles t, t + 1 and t + 2's
         if (loader) {
             if (n_top != A.K || i0 != g0) {   // it came otherwise
 #pragma unroll
@@ -511,27 +498,49 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             pos3 = position(i0 + 3);
 #pragma unroll
             for (int t = 0; t < NP; ++t)
-                row[t] = put_row(i0 + t, i0 + t < i1 && (i0 + t) * kTile + tid < n_keys ? pos_g[t] : -1, page_g[t]);
+                row[t] = row_of(i0 + t < i1 && (i0 + t) * kTile + tid < n_keys ? pos_g[t] : -1, page_g[t]);
         }
-        __syncthreads();
 
-        // copies of a tile's rows, D / 16 threads a row
-        auto gather = [&](int t, const uint8_t *src, int off) {
-            int ids[NIT];
+        // Copies of a warp's 32 keys, D / 16 threads a row: K into its swizzled tile; V's codes
+        // to where the thread that copied them finds them again.
+        const int key_l = (tid & 96) + lane / CPH, ch_l = lane % CPH;   // turn 0's key and chunk
+        auto gather_k = [&](int row) {
 #pragma unroll
-            for (int q = 0; q < NIT / 4; ++q)
-                reinterpret_cast<int4 *>(ids)[q] = reinterpret_cast<const int4 *>(rows + (t & 3) * kTile + (tid / CPH) * NIT)[q];
-            const uint8_t *from = src + (tid % CPH) * 16;
-            uint8_t *to = sm + off + sw<D>(tid / CPH, tid % CPH);   // RPT is a multiple of 8: one swizzle for all rows
+            for (int i = 0; i < NIT; ++i) {
+                const int id = __shfl_sync(0xffffffffu, row, i * RPT + lane / CPH);
+                cp_async16_or_zero(sm + C::kOffK + sw<D>(key_l + i * RPT, ch_l), A.k + (int64_t)max(id, 0) * D + ch_l * 16, id >= 0);
+            }
+        };
+        uint4 vc[NIT];   // V's codes
+        auto gather_v = [&](int row) {
 #pragma unroll
-            for (int i = 0; i < NIT; ++i)
-                cp_async16_or_zero(to + i * RPT * D, from + (int64_t)max(ids[i], 0) * D, ids[i] >= 0);
+            for (int i = 0; i < NIT; ++i) {
+                const int id = __shfl_sync(0xffffffffu, row, i * RPT + lane / CPH);
+                vc[i] = make_uint4(0, 0, 0, 0);
+                if (id >= 0) vc[i] = __ldg(reinterpret_cast<const uint4 *>(A.v + (int64_t)id * D + ch_l * 16));
+            }
+        };
+        // V(t)'s codes to fp16 (exact).  With 128 dims the threads of a row's upper half write
+        // their two chunks in the other order: in one go the two halves would meet in the banks.
+        auto widen_v = [&]() {
+            const bool flip = D == 128 && ch_l >= 4;
+#pragma unroll
+            for (int i = 0; i < NIT; ++i) {
+                const uint4 c = vc[i];
+                uint4 a, b;
+                f16_of_e4m3x4(flip ? c.z : c.x, a.x, a.y);
+                f16_of_e4m3x4(flip ? c.w : c.y, a.z, a.w);
+                f16_of_e4m3x4(flip ? c.x : c.z, b.x, b.y);
+                f16_of_e4m3x4(flip ? c.y : c.w, b.z, b.w);
+                uint8_t *to = sm + C::kOffV;
+                const int key = key_l + i * RPT, ch = 2 * ch_l + (flip ? 1 : 0);
+                *reinterpret_cast<uint4 *>(to + sw_v(key, ch)) = a;
+                *reinterpret_cast<uint4 *>(to + sw_v(key, ch ^ 1)) = b;
+            }
         };
         float ks0 = 0.f, vs0 = 0.f;
         if (loader) {
-            gather(i0, A.k, C::kOffK);
-            cp_async_commit();
-            gather(i0, A.v, C::kOffV);
+            gather_k(row[0]);
             cp_async_commit();
             if (row[0] >= 0) {
                 ks0 = __ldg(A.k_scale + (row[0] >> P.sb_shift));
@@ -567,7 +576,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             *reinterpret_cast<uint4 *>(sm + C::kOffQ + sw<D>(HQP + c / CPH, c % CPH)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         if (loader) put_scale(i0, row[0], ks0, vs0);
-        cp_async_wait<1>();   // the K tile; V's is waited for before P V
+        cp_async_wait<0>();   // the K tile
         fence_async_smem();
         __syncthreads();
 
@@ -585,13 +594,13 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             tc_commit(bar_s + ((t - i0) & 1));
         };
         auto issue_pv = [&](int t) {   // A (V^T) and B (P^T) both MN-major
-            constexpr uint32_t idesc = idesc_e4m3_f32(128, N2) | (1u << 15) | (1u << 16);
+            constexpr uint32_t idesc = idesc_f16_mn(128, HQP);
             const uint64_t vd = desc_v<D>(smem_u32(sm + C::kOffV));
-            const uint64_t pd = desc_mn_plain(smem_u32(sm + C::kOffP), N2 * 8, 128);
+            const uint64_t pd = desc_mn_plain(smem_u32(sm + C::kOffP), HQP * 16, 128);
 #pragma unroll
-            for (int kk = 0; kk < kTile / 32; ++kk)   // 32 keys: four 8-key groups
-                tc_mma_f8(tmem + 2 * SN, vd + (uint64_t)((kk * 32 * D) >> 4), pd + (uint64_t)((kk * 4 * N2 * 8) >> 4), idesc,
-                          (t == i0 && kk == 0) ? 0u : 1u);
+            for (int kk = 0; kk < kTile / 16; ++kk)   // 16 keys: two 8-key groups
+                tc_mma_f16(tmem + 2 * SN, vd + (uint64_t)((kk * 2048) >> 4), pd + (uint64_t)((kk * 2 * HQP * 16) >> 4), idesc,
+                           (t == i0 && kk == 0) ? 0u : 1u);
             tc_commit(bar_pv);
         };
         bool ok = true;
@@ -602,7 +611,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         // Only the MMA warp polls: warps that poll take issue slots from those that compute,
         // and warps that wait at a barrier do not.  It tells the loader warps when P V(t - 1) and
         // S(t + 1) are done, and the softmax warps when P V(t - 1) is.
-        constexpr int kBarSoft = 6, kBarVote = 8, kSoft = C::kThreads - 128, kBarV = 1, kBarK = 7, kLoad = 160;
+        constexpr int kBarSoft = 6, kBarVote = 8, kSoft = C::kThreads - 128, kBarV = 1, kBarK = 7, kBarKIn = 9, kLoad = 160;
         if (warp == C::kWarpMma) {
             // ------------------------------------------------------------ MMA warp
             if (elect_one()) issue_s(i0);
@@ -615,7 +624,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 if (elect_one()) issue_s(i0 + 1);
                 __syncwarp();
                 ok = ok && wait_s(i0 + 1);
-                bar_arrive_n(kBarK, kLoad);
+                if (i0 + 2 < i1) bar_arrive_n(kBarK, kLoad);
             }
             for (int t = i0; t < i1; ++t) {
                 if (__syncthreads_or(!ok)) {   // a wait ran out: everybody leaves here
@@ -632,26 +641,26 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 if (t + 1 < i1) bar_arrive_n(kBarV, kLoad);
                 if (t + 2 < i1) {
                     // Not before the vote on tile t + 1 has read its scores: reads that meet MMAs
-                    // wait.  (4 x 1024 rows of 64 heads 326 us; behind P V's end 348, right behind
-                    // P V in one go 355.)
+                    // wait.  (Behind P V's end 7 percent more for 4 x 1024 rows of 64 heads.)
                     bar_sync_n(kBarVote, kSoft);
+                    bar_sync_n(kBarKIn, kLoad);   // K(t + 2) is there
                     if (elect_one() && ok) issue_s(t + 2);
                     __syncwarp();
                     ok = ok && wait_s(t + 2);
-                    bar_arrive_n(kBarK, kLoad);
+                    if (t + 3 < i1) bar_arrive_n(kBarK, kLoad);
                 }
             }
             if (!ok && lane == 0) report(A.dev_status, SA_DEV_TIMEOUT);
         } else if (loader) {
             // ------------------------------------------------------------ loader warps
-            regs_dec<C::kRegsLoad>();
+            gather_v(row[0]);
             if (row[1] >= 0) {
                 ks0 = __ldg(A.k_scale + (row[1] >> P.sb_shift));
                 vs0 = __ldg(A.v_scale + (row[1] >> P.sb_shift));
             }
             if (i0 + 1 < i1) {
                 bar_sync_n(kBarK, kLoad);   // S(i0) is done: the K tile is free
-                gather(i0 + 1, A.k, C::kOffK);
+                gather_k(row[1]);
                 cp_async_wait_all();
                 fence_async_smem();
                 bar_arrive_n(kBarV, kLoad);
@@ -665,32 +674,37 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     vs0 = __ldg(A.v_scale + (row[2] >> P.sb_shift));
                 }
                 const int pos4 = position(t + 4);
-                if (t > i0) {
-                    bar_sync_n(kBarV, kLoad);   // P V(t - 1) is done: V(t) over V(t - 1)
-                    gather(t, A.v, C::kOffV);
+                if (t > i0) bar_sync_n(kBarV, kLoad);   // P V(t - 1) is done: V(t) over V(t - 1)
+                widen_v();
+                if (t + 1 < i1) put_scale(t + 1, row[1], ks1, vs1);
+                fence_async_smem();
+                if (__syncthreads_or(false)) {   // a wait ran out
+                    if (t + 2 < i1) bar_sync_n(kBarK, kLoad);
+                    break;
                 }
-                if (t + 1 < i1) {
+                // the next copies fly while P V(t) runs
+                if (t + 1 < i1) gather_v(row[1]);
+                if (t + 2 < i1) {
                     bar_sync_n(kBarK, kLoad);   // S(t + 1) is done: K(t + 2) over K(t + 1)
-                    if (t + 2 < i1) gather(t + 2, A.k, C::kOffK);
-                    put_scale(t + 1, row[1], ks1, vs1);
+                    gather_k(row[2]);
                 }
                 row[1] = row[2];
-                row[2] = put_row(t + 3, pos3, pg3);
+                row[2] = row_of(pos3, pg3);
                 pos3 = pos4;
                 cp_async_wait_all();
-                fence_async_smem();
-                if (__syncthreads_or(false)) break;   // a wait ran out
+                if (t + 2 < i1) {
+                    fence_async_smem();
+                    bar_arrive_n(kBarKIn, kLoad);
+                }
             }
-            regs_inc<C::kRegs>();
         } else {
             // ------------------------------------------------------------ softmax warps
-            regs_inc<C::kRegsSoft>();
             f2 l[HG / 2];
 #pragma unroll
             for (int i = 0; i < HG / 2; ++i) l[i] = 0;
             float *gmax = reinterpret_cast<float *>(sm + C::kOffMax) + h0 * 4;   // [quad][HG]
             uint32_t *flags = reinterpret_cast<uint32_t *>(sm + C::kOffFlags) + 4 * hg;   // [quad]
-            uint8_t *pbuf = sm + C::kOffP + (key >> 3) * (N2 * 8) + (key & 7) * 16 + (h0 / 16) * 128;
+            uint8_t *pbuf = sm + C::kOffP + (key >> 3) * (HQP * 16) + (key & 7) * 16 + (h0 / 8) * 128;
             float m = kLowest;   // a head a lane: its running maximum
             if (lane < HG) negm[lane] = -m;
             bool fresh = true;                         // no key yet
@@ -699,8 +713,9 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 // S(t) is done: the MMA warp waited for it before it met the last barrier
                 tc_fence_after();
                 const uint32_t s_t = lane_t + (uint32_t)(((t - i0) & 1) * SN);
-                const float *kf = sc + (t & 1) * 3 * kTile + key;
-                const f2 c2 = pk(kf[0], kf[0]), lv2 = pk(kf[kTile], kf[kTile]), iv2 = pk(kf[2 * kTile], kf[2 * kTile]);
+                const float *kf = sc + (t & 1) * 2 * kTile + key;
+                const float lv = kf[kTile], iv = lv > -CUDART_INF_F ? ex2f(-lv) : 0.f;
+                const f2 c2 = pk(kf[0], kf[0]), lv2 = pk(lv, lv), iv2 = pk(iv, iv);
                 // Scores of N heads: read from TMEM for the vote and again for P (of 32 heads the
                 // second half: keeping all of them beside 32 sums spills).
                 auto scores = [&](int c, auto &x) {
@@ -743,23 +758,23 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                         }
                     }
                     if (lane < HG) gmax[quad * HG + lane] = tm;
-                    const bool any_key = bar_or(3 + 2 * hg, 128, kf[kTile] > -CUDART_INF_F);
+                    const bool any_key = bar_or(3 + 2 * hg, 128, lv > -CUDART_INF_F);
                     if (lane < HG) tm = fmaxf(fmaxf(gmax[lane], gmax[HG + lane]), fmaxf(gmax[2 * HG + lane], gmax[3 * HG + lane]));
                     fresh = fresh && !any_key;
                     return tm;
                 };
-                if (fresh) {   // the row's first keys: references by which the largest P is 2
+                if (fresh) {   // the row's first keys: references by which the largest P is 2^kTop
                     const float tm = maxima();
                     if (lane < HG) {
-                        if (tm > kLowest) m = tm - kTop;
+                        if (tm > kLowest) m = __fsub_ru(tm, kTop);   // (up: among large numbers it is tm itself)
                         negm[lane] = -m;
                     }
                     __syncwarp();
                 }
                 // One vote of the group a tile: does any head need a new reference?
-                // (KEEP: the first 16 heads' e is kept for P.  2048 rows of 9 tiles: 92 us
-                // without, 88 with; the cluster form would spill.)
-                constexpr bool KEEP = !CL;
+                // (KEEP: the first 16 heads' e is kept for P, where registers allow: with 64
+                // heads it spills, 412 us for the padded chunk instead of 393.)
+                constexpr bool KEEP = !CL && HQP == 16;
                 f2 e0[8];
                 exponents(0, e0);
                 float top = -CUDART_INF_F;
@@ -801,13 +816,13 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     if (lane == 0) flags[quad] = heads;
                     // They go up by kStep: nothing but a bit a head has to be known of the other
                     // keys.  Where that is not enough, or lost in a large reference's rounding, to
-                    // what takes the largest P back to 2.
+                    // what takes the largest P back to 2^kTop.
                     const bool far = bar_or(3 + 2 * hg, 128, top > kRaise + kStep || (lane < HG && fabsf(m) > kCoarse));
                     const uint4 fl = *reinterpret_cast<const uint4 *>(flags);
                     heads = fl.x | fl.y | fl.z | fl.w;
                     const bool mine = (heads >> lane) & 1u;
                     float to = m + kStep, f = 1.f;
-                    if (far) to = maxima() - kTop;
+                    if (far) to = __fsub_ru(maxima(), kTop);
                     if (mine) {
                         f = ex2f(m - to);   // what the row's earlier tiles made of the head shrinks by this
                         m = to;
@@ -822,26 +837,21 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
 #pragma unroll
                         for (int i = 0; i < 4; ++i) l[c / 2 + i] = fma2(l[c / 2 + i], pk(fc[2 * i], fc[2 * i + 1]), 0);
                         if (t > i0) {
-                            uint32_t o[8], ol[8];   // both parts
+                            uint32_t o[8];
                             tmem_ld_x8(lane_t + (uint32_t)(2 * SN + c), o);
-                            tmem_ld_x8(lane_t + (uint32_t)(2 * SN + HQP + c), ol);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                o[k] = __float_as_uint(__uint_as_float(o[k]) * fc[k]);
-                                ol[k] = __float_as_uint(__uint_as_float(ol[k]) * fc[k]);
-                            }
+                            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fc[k]);
                             tmem_st8(lane_t + (uint32_t)(2 * SN + c), o);
-                            tmem_st8(lane_t + (uint32_t)(2 * SN + HQP + c), ol);
                         }
                     }
                     tmem_st_wait_all();
                     __syncwarp();
                     if (KEEP && (heads & 0xFFFFu)) exponents(0, e0);
                 }
-                // P^T as an MN-major operand without swizzle: 16-byte rows of 16 heads, the
+                // P^T as an MN-major operand without swizzle: 16-byte rows of 8 heads, the
                 // rows of 8 keys 16 bytes apart, the head chunks of a key group 128 bytes
-                // apart (first all high parts, then the low ones), key groups N2 * 8 bytes apart
+                // apart, key groups HQP * 16 bytes apart
 #pragma unroll
                 for (int c = 0; c < HG; c += 16) {
                     f2 e[8];
@@ -851,25 +861,16 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     } else {
                         exponents(c, e);
                     }
-                    uint32_t hi[4], lo[4];
+                    uint32_t p16[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {   // four heads
-                        uint32_t p16[2], h16[2];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float2 f = up(e[2 * i + k]);
-                            const float p0 = ex2f(f.x), p1 = ex2f(f.y);
-                            f2 &sum = l[c / 2 + 2 * i + k];
-                            sum = fma2(pk(p0, p1), iv2, sum);
-                            p16[k] = f16x2(p0, p1);
-                        }
-                        hi[i] = e4m3x4_of_f16(p16[0], p16[1]);
-                        f16_of_e4m3x4(hi[i], h16[0], h16[1]);
-                        // the rest (exact) times 16
-                        lo[i] = e4m3x4_of_f16(hmul2(hsub2(p16[0], h16[0]), 0x4C004C00u), hmul2(hsub2(p16[1], h16[1]), 0x4C004C00u));
+                    for (int i = 0; i < 8; ++i) {   // two heads
+                        const float2 f = up(e[i]);
+                        const float p0 = ex2f(f.x), p1 = ex2f(f.y);
+                        l[c / 2 + i] = fma2(pk(p0, p1), iv2, l[c / 2 + i]);
+                        p16[i] = f16x2(p0, p1);
                     }
-                    *reinterpret_cast<uint4 *>(pbuf + c * 8) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(pbuf + (HQP + c) * 8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    *reinterpret_cast<uint4 *>(pbuf + c * 16) = make_uint4(p16[0], p16[1], p16[2], p16[3]);
+                    *reinterpret_cast<uint4 *>(pbuf + c * 16 + 128) = make_uint4(p16[4], p16[5], p16[6], p16[7]);
                 }
                 fence_async_smem();
                 tc_fence_before();
@@ -909,21 +910,20 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             }
             bar_sync_n(kBarSoft, kSoft);   // P V of the last tile is done
             tc_fence_after();
-            // O = O_hi + O_lo / 16: a part of a row as it is into shared memory (the K and V tiles
-            // are idle by now), for the join; a row normalised and out, 64 bytes of a head a
-            // store (staged for 16-byte stores: 2048 rows 85.5 us, so 82.3)
+            // A part of a row as it is into shared memory (the K and V tiles are idle by
+            // now), for the join; a row normalised and out, 64 bytes of a head a store (staged
+            // for 16-byte stores it took 4 percent longer)
             float *part = reinterpret_cast<float *>(sm + C::kOffK) + h0 * D;
             uint16_t *out = A.out + ((int64_t)r * A.Hq + h0) * D + key;
 #pragma unroll
             for (int c = 0; c < HG; c += 8) {
-                uint32_t u[8], v[8];
+                uint32_t u[8];
                 tmem_ld_x8(lane_t + (uint32_t)(2 * SN + c), u);
-                tmem_ld_x8(lane_t + (uint32_t)(2 * SN + HQP + c), v);
                 tmem_ld_wait();
                 if (D == 128 || key < D) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const float o = fmaf(__uint_as_float(v[k]), 0.0625f, __uint_as_float(u[k]));
+                        const float o = __uint_as_float(u[k]);
                         if (CL) {
                             part[(c + k) * D + key] = o;
                         } else {
@@ -933,7 +933,6 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     }
                 }
             }
-            regs_dec<C::kRegs>();
         }
     } else if (CL && tid < HQP) {   // no share of the row
         part_ml[tid] = make_float2(kLowest, 0.f);
@@ -994,12 +993,6 @@ template <int D, int HQP, bool CL>
 sa_status launch_q8(const Params &p, int R, cudaStream_t st) {
     using C = Cfg<D, HQP>;
     if (prepare_kernel<attn_q8_kernel<D, HQP, CL>>(C::kSmem, CL) != cudaSuccess) return SA_ERR_CUDA;
-    // the warps' register shares are taken from what the launch gives its threads
-    static const int regs = [] {
-        cudaFuncAttributes f;
-        return cudaFuncGetAttributes(&f, attn_q8_kernel<D, HQP, CL>) == cudaSuccess ? f.numRegs : 0;
-    }();
-    if (regs < C::kRegs) return SA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)R * (unsigned)p.G);
     cfg.blockDim = dim3(C::kThreads);

@@ -492,8 +492,12 @@ sa_status sa_cache_append_q8(const sa_bf16 *q, int64_t ld_q, sa_bf16 *q_out,
  *   writes it with the same n_valid), out [B*T, Hq, d] bf16, lse [B*T, Hq]
  *   fp32; q, out and the caches 16-byte aligned.  Scales are read as numbers in
  *   [2^-64, 2^64] (others are taken to the nearer end).
- *   Softmax and accumulation are fp32.  No workspace: the rows of small steps
- *   are split over thread-block clusters and joined in shared memory.
+ *   Softmax and accumulation are fp32; for the P.V product the unnormalised
+ *   probabilities are rounded to fp16, off by 2^-11 of their value or 2^-32 of
+ *   the head's largest p * v_scale, whichever is more; q is taken with 2^-18 of
+ *   the row's largest value or exactly; out is rounded to bf16 (nearest even).
+ *   No workspace: the rows of small steps are split over thread-block clusters
+ *   and joined in shared memory.
  *   Errors: K + W = 0 is SA_ERR_INVALID_ARG; SA_ERR_UNSUPPORTED if B * S_max
  *   or pool_pages * 64 exceeds INT32_MAX rows, or K + W > 524288; device
  *   SA_DEV_INDEX for an n_valid outside the cache (that row is treated as
