@@ -73,6 +73,7 @@ namespace {
 constexpr int kTile = 128;                  // keys per tile (MMA M)
 constexpr float kTop = 8.f, kRaise = 15.75f; // log2 of a row's largest P at first, and of what it may grow to
 constexpr float kStep = 8.f;                // how far a head's reference goes up then
+constexpr float kSmallV = -30.f;            // log2 of the value scales from which P may vanish before the weight does
 constexpr float kLowest = -3.4028235e38f;   // running maximum of a head that has met no finite score yet
 constexpr float kCoarse = 8388608.f;        // a reference from 2^23 on is not moved by steps
 constexpr int kSmemSm = 233472;             // shared memory of an SM, 1 KB of it reserved per CTA
@@ -148,6 +149,11 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // Arrive at barrier `id` of `n` threads without waiting for it; wait for it; wait and return the OR of a predicate.
 __device__ __forceinline__ void bar_arrive_n(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
@@ -200,6 +206,9 @@ __device__ __forceinline__ float redux_max(float x) {   // NaN counts as absent
 __device__ __forceinline__ void cp_async16_or_zero(void *smem_dst, const void *gsrc, bool some) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(gsrc), "r"(some ? 16 : 0)
                  : "memory");
+}
+__device__ __forceinline__ void tmem_ld_x2(uint32_t taddr, uint32_t (&r)[2]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(taddr));
 }
 // Two f32 rounded to f16 (lo in the low half), and f16 pairs to and from e4m3.
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
@@ -706,6 +715,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             uint32_t *flags = reinterpret_cast<uint32_t *>(sm + C::kOffFlags) + 4 * hg;   // [quad]
             uint8_t *pbuf = sm + C::kOffP + (key >> 3) * (HQP * 16) + (key & 7) * 16 + (h0 / 8) * 128;
             float m = kLowest;   // a head a lane: its running maximum
+            float l_small = 0.f; // (clusters) and its sum over this warp's keys of small value scales
             if (lane < HG) negm[lane] = -m;
             bool fresh = true;                         // no key yet
             bar_sync_n(kBarSoft, kSoft);               // S(i0) is done
@@ -714,7 +724,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 tc_fence_after();
                 const uint32_t s_t = lane_t + (uint32_t)(((t - i0) & 1) * SN);
                 const float *kf = sc + (t & 1) * 2 * kTile + key;
-                const float lv = kf[kTile], iv = lv > -CUDART_INF_F ? ex2f(-lv) : 0.f;
+                const float lv = kf[kTile], iv = lv >= kSmallV ? ex2f(-lv) : 0.f;
                 const f2 c2 = pk(kf[0], kf[0]), lv2 = pk(lv, lv), iv2 = pk(iv, iv);
                 // Scores of N heads: read from TMEM for the vote and again for P (of 32 heads the
                 // second half: keeping all of them beside 32 sums spills).
@@ -824,7 +834,10 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     float to = m + kStep, f = 1.f;
                     if (far) to = __fsub_ru(maxima(), kTop);
                     if (mine) {
-                        f = ex2f(m - to);   // what the row's earlier tiles made of the head shrinks by this
+                        // What the row's earlier tiles made of the head shrinks by f^2: the step may be
+                        // that of two value scales, 2^128, and the sum is not of contributions but weights.
+                        f = ex2f(0.5f * (m - to));
+                        if (CL) l_small *= f * f;
                         m = to;
                         negm[lane] = -m;
                     }
@@ -835,13 +848,16 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
 #pragma unroll
                         for (int i = 0; i < 8; ++i) fc[i] = __shfl_sync(0xffffffffu, f, c + i);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) l[c / 2 + i] = fma2(l[c / 2 + i], pk(fc[2 * i], fc[2 * i + 1]), 0);
+                        for (int i = 0; i < 4; ++i) {
+                            const f2 f2i = pk(fc[2 * i], fc[2 * i + 1]);
+                            l[c / 2 + i] = mul2(mul2(l[c / 2 + i], f2i), f2i);
+                        }
                         if (t > i0) {
                             uint32_t o[8];
                             tmem_ld_x8(lane_t + (uint32_t)(2 * SN + c), o);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fc[k]);
+                            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fc[k] * fc[k]);
                             tmem_st8(lane_t + (uint32_t)(2 * SN + c), o);
                         }
                     }
@@ -872,6 +888,44 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     *reinterpret_cast<uint4 *>(pbuf + c * 16) = make_uint4(p16[0], p16[1], p16[2], p16[3]);
                     *reinterpret_cast<uint4 *>(pbuf + c * 16 + 128) = make_uint4(p16[4], p16[5], p16[6], p16[7]);
                 }
+                // A key of a small value scale: its P may be next to nothing beside those of large
+                // ones (down to 2^-128), its weight not, so that one is computed by itself.
+                // (Rare, but its code has to be chosen: in a cluster, where each CTA runs the loop's
+                // body a few times, a short one, a head a lane; else one that takes no register.
+                // 16 paged rows of 2560 keys 14.5 us, the other way 16.8; padded chunk 381 and 483.)
+                const bool small = lv > -CUDART_INF_F && lv < kSmallV;
+                if (__any_sync(0xffffffffu, small)) {
+                    if constexpr (CL) {
+#pragma unroll 1
+                        for (int c = 0; c < HG; c += 2) {
+                            uint32_t u[2][2] = {};
+                            tmem_ld_x2(s_t + (uint32_t)c, u[0]);
+                            if (C::kSide) tmem_ld_x2(s_t + (uint32_t)(HQP + c), u[1]);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                float w = __uint_as_float(u[0][i]);
+                                if (C::kSide) w += __uint_as_float(u[1][i]);
+                                w = small ? ex2f(fmaf(w, kf[0], lv) + negm[c + i] - lv) : 0.f;
+#pragma unroll
+                                for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+                                if (lane == c + i) l_small += w;
+                            }
+                        }
+                    } else {
+                        const float off = small ? lv : CUDART_INF_F;
+#pragma unroll
+                        for (int c = 0; c < HG; c += 8) {
+                            f2 e[4];
+                            exponents(c, e);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 f = up(e[i]);
+                                l[c / 2 + i] = add2(l[c / 2 + i], pk(ex2f(f.x - off), ex2f(f.y - off)));
+                            }
+                        }
+                    }
+                }
                 fence_async_smem();
                 tc_fence_before();
                 if (__syncthreads_or(false)) break;   // a wait ran out
@@ -895,7 +949,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 }
             }
             if (HG == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
-            if (lane < HG) gmax[quad * HG + lane] = v[0];
+            if (lane < HG) gmax[quad * HG + lane] = CL ? v[0] + l_small : v[0];
             bar_sync_n(3 + 2 * hg, 128);
             if (lane < HG) {
                 const float L = (gmax[lane] + gmax[HG + lane]) + (gmax[2 * HG + lane] + gmax[3 * HG + lane]);
@@ -963,11 +1017,11 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             if (lane < G) dsmem_ld(in_cta(sm, (uint32_t)lane) + C::kOffEpi + h * 8, ml);
             fetch(0);
             const bool some = ml[1] != 0.f;   // (a part without keys wrote nothing)
-            const float m = redux_max(some ? ml[0] : kLowest), f = some ? ex2f(ml[0] - m) : 0.f;
-            float L = some ? f * ml[1] : 0.f;
+            const float m = redux_max(some ? ml[0] : kLowest), fh = some ? ex2f(0.5f * (ml[0] - m)) : 0.f;   // (as in a raise)
+            float L = some ? fh * ml[1] * fh : 0.f;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-            const float w = L == 0.f ? 0.f : f * rcp(L);
+            const float w = L == 0.f ? 0.f : fh * rcp(L) * fh;
             float o[V] = {};
             for (int c0 = 0; c0 < G; c0 += AT) {
                 if (c0 > 0) fetch(c0);

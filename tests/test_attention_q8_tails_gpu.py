@@ -114,3 +114,22 @@ def test_equal_keys_far_below_a_sink_share_its_tail(sa):
     out, _ = run(sa, x, 1, 1, 0, n, sb)
     o, _, aw, rel = want(x, sb, torch.arange(n), 0, d ** -0.5)
     assert ((out[0] - o).abs() <= 2.0 ** -8 * o.abs() + (2.0 ** -10 + rel) * aw).all()
+
+
+@pytest.mark.parametrize("Hq,T", [(16, 1), (64, 1), (16, 300), (40, 300)])
+@pytest.mark.parametrize("order", ["small first", "large first", "in turn"])
+def test_keys_of_the_smallest_value_scale_weigh_as_much_as_any(sa, Hq, T, order):
+    """Value scales at both ends of their range (2^64 and 2^-64) under scores of one size: the small ones' keys count in
+    the row sum, whichever the row meets first, in one tile, in tiles apart and in the parts of a cluster."""
+    n, sb, d, W = 1280, 64, 128, 1280
+    x = sink_inputs(T, Hq, d, n, sb, 1.0, 1.0, 0, seed=50 + T)
+    x["q"][..., 0] = 0   # no sink
+    blocks = n // sb
+    small = {"small first": torch.arange(blocks) < blocks // 2, "large first": torch.arange(blocks) >= blocks // 2,
+             "in turn": torch.arange(blocks) % 2 == 1}[order]
+    x["vs"] = torch.where(small, 2.0 ** -64, 2.0 ** 64).float()
+    out, lse = run(sa, x, 1, T, 0, W, sb)
+    for r in sorted({0, T // 2, T - 1}):
+        o, z, aw, rel = want(x, sb, torch.arange(int(x["nv"][r])), r, d ** -0.5)
+        assert ((lse[r] - z).abs() <= rel + 2.0 ** -22 * z.abs()).all(), float((lse[r] - z).abs().max())
+        assert ((out[r] - o).abs() <= 2.0 ** -8 * o.abs() + (2.0 ** -10 + rel) * aw).all()
