@@ -20,6 +20,7 @@ per C-ABI call, so that callers can time each kernel; ``run`` executes them.
 
 from __future__ import annotations
 
+import contextlib
 import math
 
 import torch
@@ -155,7 +156,9 @@ class KVCache:
     scale_block tokens (else bf16); index_fp8: e4m3 index keys.
     Positions: pairs of the first rot_dim dims (default all) turn by
     p * inv_freq[i]; inv_freq defaults to theta^(-2i / rot_dim).
-    interleaved: pairs (2i, 2i + 1) instead of (i, i + rot_dim / 2)."""
+    interleaved: pairs (2i, 2i + 1) instead of (i, i + rot_dim / 2).
+    The caches are zeroed on the stream that is current here; an append on
+    another waits for it first (stream.wait_stream)."""
 
     def __init__(self, B, d, D_I, S_max=0, paged=False, max_pages=0, pool_pages=0, q8=False, scale_block=64,
                  index_fp8=False, rot_dim=None, theta=10000.0, inv_freq=None, interleaved=False, device="cuda"):
@@ -200,7 +203,7 @@ class KVCache:
         """Write the new tokens' rotated keys, values and index keys ([B*T, *])
         to their slots (row b*T + t at position n_valid[b*T + t] - 1, 0:
         padding) and return the rotated queries (q [B*T, Hq, d], q_out or a new
-        tensor; None when q is None)."""
+        tensor of `stream`; None when q is None)."""
         R, d = self.B * T, self.d
         if self.paged and page_table is None:
             raise ValueError("a paged cache is appended to through its page table")
@@ -208,7 +211,9 @@ class KVCache:
         if q is not None and q.numel() != R * Hq * d:
             raise ValueError("q holds whole heads of %d values for each of %d rows" % (d, R))
         if q is not None and q_out is None:
-            q_out = torch.zeros((R, Hq, d), dtype=torch.bfloat16, device=q.device)
+            # on the stream that writes it: zeros of another could land after the kernel
+            with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+                q_out = torch.zeros((R, Hq, d), dtype=torch.bfloat16, device=q.device)
         (q, ld_q), (k, ld_k) = self._rows(q, R, Hq * d), self._rows(k, R, d)
         (v, ld_v), (kI, ld_kI) = self._rows(v, R, d), self._rows(kI, R, self.D_I)
         status = self.dev_status if dev_status is None else dev_status
