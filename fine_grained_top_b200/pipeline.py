@@ -194,6 +194,8 @@ class KVCache:
         if t is None:
             return None, 0
         if t.is_contiguous():
+            if t.numel() != R * width:   # rows of another width, or another number of them
+                raise ValueError("%d values where %d rows of %d are new" % (t.numel(), R, width))
             return t, width
         if t.dim() != 2 or tuple(t.shape) != (R, width) or t.stride(1) != 1:
             raise ValueError("new rows are contiguous, or [rows, %d] slices of wider rows" % width)
@@ -207,6 +209,8 @@ class KVCache:
         R, d = self.B * T, self.d
         if self.paged and page_table is None:
             raise ValueError("a paged cache is appended to through its page table")
+        if n_valid.numel() != R:
+            raise ValueError("n_valid has %d entries where %d rows are new" % (n_valid.numel(), R))
         Hq = q.numel() // (R * d) if q is not None and R > 0 else 1
         if q is not None and q.numel() != R * Hq * d:
             raise ValueError("q holds whole heads of %d values for each of %d rows" % (d, R))
