@@ -64,6 +64,8 @@ SIGNATURES = {
     "sa_coarse_block_counts": (_i32, [_i32, _i32, _i32, _vp, _vp]),
     "sa_expand_blocks": (_i32, [_vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp]),
     "sa_selftest_wait_timeout": (_i32, [_i32, _vp, _vp]),
+    "sa_selftest_attn_q8_timeout": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _f32, _vp, _i32, _i32, _i32, _vp,
+                                           _vp]),
 }
 
 
@@ -393,6 +395,18 @@ def sa_dev_status_decode(word: int) -> int:
 
 def sa_version() -> int:
     return int(_lib.sa_version())
+
+
+def sa_selftest_attn_q8_timeout(q, k_cache, v_cache, k_scale, v_scale, S_max, n_valid, B, Hq, scale, out, ctas, lost,
+                                limit_us, dev_status, stream=None):
+    t, n = _types(), B * S_max
+    bf, dev = t.bf, q.get_device()
+    _refuse(dev, (("q", q, bf, B * Hq * 128), ("k_cache", k_cache, t.f8, n * 128), ("v_cache", v_cache, t.f8, n * 128),
+                  ("k_scale", k_scale, t.f32, n // 64), ("v_scale", v_scale, t.f32, n // 64), ("n_valid", n_valid, t.i32, B),
+                  ("out", out, bf, B * Hq * 128), ("dev_status", dev_status, t.i32, 1)))
+    _check(_lib.sa_selftest_attn_q8_timeout(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), S_max,
+                                            _ptr(n_valid), B, Hq, scale, _ptr(out), ctas, lost, int(limit_us),
+                                            _ptr(dev_status), _stream(stream)), "sa_selftest_attn_q8_timeout")
 
 
 def sa_selftest_wait_timeout(limit_us, dev_status, stream=None):

@@ -85,6 +85,8 @@ struct Params {
     int hpr;              // heads that a CTA of a cluster joins
     int sb_shift;         // log2 of the tokens a scale
     float scale_log2;
+    unsigned long long limit_ns;   // health check: of every wait
+    int lost;                      // health check: S (even) or P V (odd) of this half of a tile of row 0 never comes
 };
 
 template <int D_, int HQP_>
@@ -295,7 +297,9 @@ __host__ __device__ constexpr uint32_t idesc_f16_mn(int M, int N) {
 
 // CL: a cluster shares the row (the two forms are apart to keep the code, and the
 // instruction cache it needs, small).
-template <int D, int HQP, bool CL>
+// CHECK: the health check's form, whose waits take their limit from the call and one of
+// whose MMAs is not issued.
+template <int D, int HQP, bool CL, bool CHECK = false>
 __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) attn_q8_kernel(Params P) {
     using C = Cfg<D, HQP>;
     constexpr int NT = C::kThreads, HG = C::HG, SN = C::SN;
@@ -303,8 +307,8 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     float *sc = reinterpret_cast<float *>(sm + C::kOffSc);
     float2 *part_ml = reinterpret_cast<float2 *>(sm + C::kOffEpi);   // a part's m and l
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + C::kOffMisc);
-    uint64_t *bar_s = bar, *bar_pv = bar + 2;   // S(t) done, one for each S buffer; P V(t) done
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 3);
+    uint64_t *bar_s = bar, *bar_pv = bar + 2, *bar_drain = bar + 3;   // S(t) done, one for each S buffer; P V(t) done; all MMAs
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 4);
     int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
     uint2 *found = reinterpret_cast<uint2 *>(sm + C::kOffMisc + 64);   // a warp's first entry not taken, its largest |q|
 
@@ -371,6 +375,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         mbar_init(bar_s, 1);
         mbar_init(bar_s + 1, 1);
         mbar_init(bar_pv, 1);
+        mbar_init(bar_drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -589,7 +594,9 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         fence_async_smem();
         __syncthreads();
 
+        auto lost = [&](int t, int what) { return CHECK && r == 0 && rank == 0 && P.lost == 2 * (t - i0) + what; };
         auto issue_s = [&](int t) {   // both parts of Q into the same columns
+            if (lost(t, 0)) return;
             constexpr uint32_t idesc = idesc_e4m3_f32(128, SN);
             const uint64_t kd = smem_desc(smem_u32(sm + C::kOffK), 8 * D, D == 128 ? 2 : 4);
             const uint64_t qd = smem_desc(smem_u32(sm + C::kOffQ), 8 * D, D == 128 ? 2 : 4);
@@ -603,6 +610,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             tc_commit(bar_s + ((t - i0) & 1));
         };
         auto issue_pv = [&](int t) {   // A (V^T) and B (P^T) both MN-major
+            if (lost(t, 1)) return;
             constexpr uint32_t idesc = idesc_f16_mn(128, HQP);
             const uint64_t vd = desc_v<D>(smem_u32(sm + C::kOffV));
             const uint64_t pd = desc_mn_plain(smem_u32(sm + C::kOffP), HQP * 16, 128);
@@ -615,8 +623,19 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         bool ok = true;
         // P V(t) is phase t - i0 of its barrier; S(t) may end while some warp still looks for
         // the end of S(t - 1), so each S buffer has a barrier of its own
-        auto wait_s = [&](int t) { return mbar_wait(bar_s + ((t - i0) & 1), (uint32_t)((t - i0) >> 1) & 1u, abort_flag); };
-        auto wait_pv = [&](int t) { return mbar_wait(bar_pv, (uint32_t)(t - i0) & 1u, abort_flag); };
+        // A wait that runs out first waits for all MMAs that were issued (with a limit again):
+        // what comes after it reuses their tiles and gives their TMEM back.  None is issued then.
+        auto waited = [&](uint64_t *which, uint32_t parity) {
+            const unsigned long long limit = CHECK ? P.limit_ns : kWaitLimitNs;
+            if (__all_sync(0xffffffffu, mbar_wait(which, parity, abort_flag, limit))) return true;
+            if (elect_one()) tc_commit(bar_drain);
+            __syncwarp();
+            int none = 0;
+            mbar_wait(bar_drain, 0, &none);
+            return false;
+        };
+        auto wait_s = [&](int t) { return waited(bar_s + ((t - i0) & 1), (uint32_t)((t - i0) >> 1) & 1u); };
+        auto wait_pv = [&](int t) { return waited(bar_pv, (uint32_t)(t - i0) & 1u); };
         // Only the MMA warp polls: warps that poll take issue slots from those that compute,
         // and warps that wait at a barrier do not.  It tells the loader warps when P V(t - 1) and
         // S(t + 1) are done, and the softmax warps when P V(t - 1) is.
@@ -630,7 +649,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
             if (i0 + 1 < i1) {
                 bar_arrive_n(kBarK, kLoad);  // the K tile is free
                 bar_sync_n(kBarV, kLoad);    // K(i0 + 1) is there
-                if (elect_one()) issue_s(i0 + 1);
+                if (elect_one() && ok) issue_s(i0 + 1);
                 __syncwarp();
                 ok = ok && wait_s(i0 + 1);
                 if (i0 + 2 < i1) bar_arrive_n(kBarK, kLoad);
@@ -1043,10 +1062,10 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     }
 }
 
-template <int D, int HQP, bool CL>
+template <int D, int HQP, bool CL, bool CHECK = false>
 sa_status launch_q8(const Params &p, int R, cudaStream_t st) {
     using C = Cfg<D, HQP>;
-    if (prepare_kernel<attn_q8_kernel<D, HQP, CL>>(C::kSmem, CL) != cudaSuccess) return SA_ERR_CUDA;
+    if (prepare_kernel<attn_q8_kernel<D, HQP, CL, CHECK>>(C::kSmem, CL) != cudaSuccess) return SA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)R * (unsigned)p.G);
     cfg.blockDim = dim3(C::kThreads);
@@ -1058,7 +1077,17 @@ sa_status launch_q8(const Params &p, int R, cudaStream_t st) {
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = CL ? 1 : 0;
-    return cuda_ok(cudaLaunchKernelEx(&cfg, attn_q8_kernel<D, HQP, CL>, p));
+    return cuda_ok(cudaLaunchKernelEx(&cfg, attn_q8_kernel<D, HQP, CL, CHECK>, p));
+}
+
+// What follows from the call and p.G.
+void fill(Params &p, const AttnQ8Args &a) {
+    p.a = a;
+    p.inv_G = ((1u << 20) + p.G - 1) / p.G;
+    p.hpr = (a.Hq + p.G - 1) / p.G;
+    p.sb_shift = 0;
+    while ((1 << p.sb_shift) < a.scale_block) ++p.sb_shift;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
 }
 
 // How many clusters of G of these CTAs the device runs at once, one CTA an SM
@@ -1097,8 +1126,7 @@ sa_status launch_q8_rows(const AttnQ8Args &a, cudaStream_t st) {
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return SA_ERR_CUDA;
-    Params p;
-    p.a = a;
+    Params p = {};
     const int R = a.B * a.T;
     const int tiles = (int)std::min<int64_t>(((int64_t)a.K + a.W + kTile - 1) / kTile, ((int64_t)a.S_max + kTile - 1) / kTile);
     // CTAs a row.  In units of one tile's time in a cluster (1.0 us with 16 heads, 1.9
@@ -1122,11 +1150,7 @@ sa_status launch_q8_rows(const AttnQ8Args &a, cudaStream_t st) {
             p.G = G;
         }
     }
-    p.inv_G = ((1u << 20) + p.G - 1) / p.G;
-    p.hpr = (a.Hq + p.G - 1) / p.G;
-    p.sb_shift = 0;
-    while ((1 << p.sb_shift) < a.scale_block) ++p.sb_shift;
-    p.scale_log2 = a.scale * 1.4426950408889634f;
+    fill(p, a);
     return p.G > 1 ? launch_q8<D, HQP, true>(p, R, st) : launch_q8<D, HQP, false>(p, R, st);
 }
 
@@ -1138,6 +1162,15 @@ sa_status launch_q8_heads(const AttnQ8Args &a, cudaStream_t st) {
 }
 
 }  // namespace
+
+sa_status launch_attn_q8_check(const AttnQ8Args &a, int ctas, int lost, unsigned long long limit_ns, cudaStream_t st) {
+    Params p = {};
+    p.G = ctas;
+    fill(p, a);
+    p.limit_ns = limit_ns;
+    p.lost = lost;
+    return ctas > 1 ? launch_q8<128, 16, true, true>(p, a.B, st) : launch_q8<128, 16, false, true>(p, a.B, st);
+}
 
 sa_status launch_attn_q8(const AttnQ8Args &a, cudaStream_t st) {
     return a.d == 128 ? launch_q8_heads<128>(a, st) : launch_q8_heads<64>(a, st);

@@ -40,6 +40,8 @@ struct AttnQ8Args {
     int *dev_status;
 };
 sa_status launch_attn_q8(const AttnQ8Args &a, cudaStream_t st);
+// The same with `ctas` CTAs a row, whose waits give up after limit_ns, one for an MMA that never comes (d 128, Hq <= 16).
+sa_status launch_attn_q8_check(const AttnQ8Args &a, int ctas, int lost, unsigned long long limit_ns, cudaStream_t st);
 
 // Cache rules shared by the append and the 8-bit attention: SA_OK when the
 // cache's sizes are within limits.

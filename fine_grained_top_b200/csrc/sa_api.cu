@@ -374,6 +374,24 @@ sa_status sa_sparse_attn_q8(const sa_bf16 *q, const sa_e4m3 *k_cache, const sa_e
     });
 }
 
+sa_status sa_selftest_attn_q8_timeout(const sa_bf16 *q, const sa_e4m3 *k_cache, const sa_e4m3 *v_cache,
+                                      const float *k_scale, const float *v_scale, int S_max, const int32_t *n_valid,
+                                      int B, int Hq, float scale, sa_bf16 *out, int ctas, int lost, int limit_us,
+                                      int *dev_status, sa_stream stream) {
+    if (limit_us <= 0 || limit_us > 1000000 || !dev_status || B < 1 || B > 1024 || ctas < 1 || ctas > 16 || lost < 0 ||
+        Hq < 1 || Hq > 16 || S_max < 64 || S_max % 64 || S_max > 65536)
+        return SA_ERR_INVALID_ARG;
+    if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !n_valid || !out) return SA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return SA_ERR_INVALID_ARG;
+    return guarded([&] {
+        AttnQ8Args a = {};
+        a.q = q; a.k = k_cache; a.v = v_cache; a.k_scale = k_scale; a.v_scale = v_scale; a.scale_block = 64;
+        a.S_max = S_max; a.n_valid = n_valid; a.W = S_max; a.B = B; a.T = 1; a.Hq = Hq; a.d = 128; a.scale = scale;
+        a.out = out; a.dev_status = dev_status;
+        return launch_attn_q8_check(a, ctas, lost, (unsigned long long)limit_us * 1000ull, cs(stream));
+    });
+}
+
 sa_status sa_call(sa_call_entry entry, const void *words, int n_words) {
     if (!words) return SA_ERR_INVALID_ARG;
     switch (entry) {

@@ -567,6 +567,22 @@ sa_status sa_expand_blocks(const int32_t *blocks, int T, int S, int keep,
 sa_status sa_selftest_wait_timeout(int limit_us, int *dev_status,
                                    sa_stream stream);
 
+/* The same for the pipeline of sa_sparse_attn_q8: attention of B rows (d 128,
+ * Hq <= 16, every cached token of a contiguous cache, scale blocks of 64) in
+ * which one product of row 0 is never issued: S (lost even) or P.V (odd) of
+ * tile lost / 2 of its first CTA, `ctas` CTAs (1 .. 16) sharing a row.  The
+ * wait for it gives up after limit_us; the row's out is then unspecified, the
+ * other rows' are as ever.  *dev_status holds SA_DEV_TIMEOUT if the row has
+ * such a tile.  S_max 64 .. 65536, a multiple of 64; B <= 1024. */
+sa_status sa_selftest_attn_q8_timeout(const sa_bf16 *q, const sa_e4m3 *k_cache,
+                                      const sa_e4m3 *v_cache,
+                                      const float *k_scale,
+                                      const float *v_scale, int S_max,
+                                      const int32_t *n_valid, int B, int Hq,
+                                      float scale, sa_bf16 *out, int ctas,
+                                      int lost, int limit_us, int *dev_status,
+                                      sa_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
