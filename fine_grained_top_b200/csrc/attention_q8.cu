@@ -11,7 +11,10 @@
 //   O^T += V^T P^T     M = d, N = heads, K = 128 keys            -> TMEM
 // S takes the codes as they lie in the cache (tcgen05 kind::f8f6f4, e4m3 x e4m3
 // products are exact) and q split into two e4m3 parts: q 2^-e = q_hi + q_lo (exact for
-// a bf16 q down to 2^-10 of the row's largest value, below it off by 2^-18 of that).
+// a bf16 q down to 2^-10 of the row's largest value, below it off by 2^-18 of that).  If
+// heads lie more than 2^6 apart each has its own e, and its scores are brought to the row's
+// in TMEM before they are read (a row of such heads takes longer, the others 1 to 4 percent
+// for the question).
 // P V is a product of fp16 (kind::f16): V's codes are widened on the way (exactly), and
 // P is rounded once.  P has to keep its precision over many orders of magnitude: a key
 // that takes most of the weight with next to no value of its own (an attention sink)
@@ -111,8 +114,9 @@ struct Cfg {
     static constexpr int kOffNegM = kOffMax + 4 * HQP * 4;            // [softmax warp][HG] minus the running maxima
     static constexpr int kOffEpi = kOffNegM + 4 * HQP * 4;            // a part's m and l [HQP][2]
     static constexpr int kOffFlags = kOffEpi + 2 * HQP * 4;  // [group][4] heads to raise, by eights
-    static constexpr int kOffMisc = kOffFlags + NG * 16;
-    static constexpr int kUsed = kOffMisc + 64 + 16 * 8;
+    static constexpr int kOffQs = kOffFlags + NG * 16;                // [HQP] the heads' factors
+    static constexpr int kOffMisc = kOffQs + HQP * 4;
+    static constexpr int kUsed = kOffMisc + 64 + 16 * 16;
     static constexpr uint32_t kTmemCols = 2 * SN + HQP <= 64 ? 64 : (2 * SN + HQP <= 128 ? 128 : 256);   // two S buffers, O
     // CTAs wait for TMEM columns while others of their cluster wait for them, so
     // whatever shares an SM must fit its 512 columns: shared memory in proportion.
@@ -319,7 +323,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     uint64_t *bar_s = bar, *bar_pv = bar + 2, *bar_drain = bar + 3;   // S(t) done, one for each S buffer; P V(t) done; all MMAs
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 4);
     int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
-    uint2 *found = reinterpret_cast<uint2 *>(sm + C::kOffMisc + 64);   // a warp's first entry not taken, its largest |q|
+    uint4 *found = reinterpret_cast<uint4 *>(sm + C::kOffMisc + 64);   // a warp's first entry not taken, its heads' largest and least |q|
 
     const AttnQ8Args &A = P.a;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -370,6 +374,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         pos_g[t] = loader && kk < A.K ? __ldg(trow + kk) : -1;
     }
     uint4 qv[2 * NQ];
+    uint32_t q_head[NQ] = {};   // the largest |q| of each chunk's head
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
         const int c = tid + i * NT;
@@ -446,11 +451,13 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         if (rank == 0 && bad_idx) report(A.dev_status, SA_DEV_INDEX);
         if (rank == 0 && bad_ord) report(A.dev_status, SA_DEV_ORDER);
         first_out = (int)__reduce_min_sync(0xffffffffu, (unsigned)first_out);
-        auto largest_q = [&](uint32_t below) {   // |q| in bf16 bits; `below`: of those under it
+        // the heads' largest |q| in bf16 bits, a head's chunks lying side by side; `below`: of those under it
+        auto largest_q = [&](int i, uint32_t below) {
             uint32_t mx = 0;
 #pragma unroll
-            for (int i = 0; i < 2 * NQ; ++i) {
-                const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+            for (int j = 0; j < 2; ++j) {
+                const uint4 v = qv[2 * i + j];
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint32_t t = w[k] & 0x7FFF7FFFu;
@@ -458,19 +465,35 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                     mx = __vmaxu2(mx, t);
                 }
             }
-            return __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
+            mx = max(mx & 0xFFFFu, mx >> 16);
+#pragma unroll
+            for (int o = 1; o < CPH; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            return mx;
         };
-        uint32_t mx = largest_q(0), odd = mx >= 0x7F80u;
-        if (odd) mx = largest_q(0x7F807F80u);   // an infinite or NaN one: the largest finite
-        if (lane == 0) found[warp] = make_uint2((unsigned)first_out, mx | odd << 16);
+        uint32_t most = 0, least = 0xFFFFu, odd = 0;   // over the warp's heads with values
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            q_head[i] = largest_q(i, 0);
+            if (__any_sync(0xffffffffu, q_head[i] >= 0x7F80u)) {   // an infinite or NaN one: the largest finite
+                odd = 1;
+                q_head[i] = largest_q(i, 0x7F807F80u);
+            }
+            most = max(most, q_head[i]);
+            if (q_head[i]) least = min(least, q_head[i]);
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        least = __reduce_min_sync(0xffffffffu, least);
+        if (lane == 0) found[warp] = make_uint4((unsigned)first_out, most, least, odd);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);   // two S buffers (SN columns each), O (HQP columns)
-    const uint2 part = found[min(lane, NT / 32 - 1)];
+    const uint4 part = found[min(lane, NT / 32 - 1)];
     const int n_top = p >= 0 ? (int)__reduce_min_sync(0xffffffffu, part.x) : 0;
-    const uint32_t q_max = __reduce_max_sync(0xffffffffu, part.y & 0xFFFFu), q_odd = __any_sync(0xffffffffu, part.y >> 16);
+    const uint32_t q_max = __reduce_max_sync(0xffffffffu, part.y), q_odd = __any_sync(0xffffffffu, part.w);
+    // Heads 2^6 apart: each has an exponent of its own then, and its scores a factor
+    const bool mixed = __reduce_min_sync(0xffffffffu, part.z) + (6u << 7) < q_max;
     const int n_keys = p >= 0 ? n_top + (p - w0 + 1) : 0;
     const int n_tiles = (n_keys + kTile - 1) / kTile;
     const int i0 = by_G(n_tiles * rank), i1 = by_G(n_tiles * (rank + 1));
@@ -481,12 +504,13 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     const int key = quad * 32 + lane;                     // TMEM lane: key (S^T) or head dim (O^T)
     const uint32_t lane_t = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)h0;
     float *negm = reinterpret_cast<float *>(sm + C::kOffNegM) + (hg * 4 + quad) * HG;   // this warp's copy
+    float *q_scale = reinterpret_cast<float *>(sm + C::kOffQs);   // (mixed) the heads' exponents against the row's
 
     if (i0 < i1) {
         // the largest value's power of two, so that it lies in (224, 448] (a mantissa beyond
         // 1.75 carries into the exponent); at least 2^-120
-        const int e2 = max(-120, (int)(((q_max << 16) + 0x1FFFFFu) >> 23) - 135);
-        const float down = __int_as_float((127 - e2) << 23);
+        auto exponent_of = [](uint32_t q) { return max(-120, (int)(((q << 16) + 0x1FFFFFu) >> 23) - 135); };
+        const int e2 = exponent_of(q_max);
         const float factor = __int_as_float((e2 + 127) << 23) * P.scale_log2;
 
         constexpr int RPT = 32 / CPH, NIT = 32 / RPT;   // rows that a loader warp copies at once, turns for its 32
@@ -575,6 +599,9 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
         for (int i = 0; i < NQ; ++i) {
             const int c = tid + i * NT;
             if (c >= HQP * CPH) break;
+            const int eh = mixed ? exponent_of(q_head[i]) : e2;
+            const float down = __int_as_float((127 - eh) << 23);
+            if (mixed && c % CPH == 0) q_scale[c / CPH] = eh - e2 < -126 ? 0.f : __int_as_float((eh - e2 + 127) << 23);
             const uint4 q0 = qv[2 * i], q1 = qv[2 * i + 1];
             const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
             uint32_t hi[4], lo[4];
@@ -751,6 +778,18 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
                 const float *kf = sc + (t & 1) * 2 * kTile + key;
                 const float lv = kf[kTile], iv = lv >= kSmallV ? ex2f(-lv) : 0.f;
                 const f2 c2 = pk(kf[0], kf[0]), lv2 = pk(lv, lv), iv2 = pk(iv, iv);
+                if (mixed) {   // S in the row's exponent, in place (unrolled: a loop here costs the whole one registers)
+#pragma unroll
+                    for (int c = 0; c < (C::kSide ? 2 : 1) * HG; c += 8) {
+                        uint32_t u[8];
+                        tmem_ld_x8(s_t + (uint32_t)c, u);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * q_scale[h0 + (c + i) % HG]);
+                        tmem_st8(s_t + (uint32_t)c, u);
+                    }
+                    tmem_st_wait_all();
+                }
                 // Scores of N heads: read from TMEM for the vote and again for P (of 32 heads the
                 // second half: keeping all of them beside 32 sums spills).
                 auto scores = [&](int c, auto &x) {

@@ -494,8 +494,9 @@ sa_status sa_cache_append_q8(const sa_bf16 *q, int64_t ld_q, sa_bf16 *q_out,
  *   [2^-64, 2^64] (others are taken to the nearer end).
  *   Softmax and accumulation are fp32; for the P.V product the unnormalised
  *   probabilities are rounded to fp16, off by 2^-11 of their value or 2^-32 of
- *   the head's largest p * v_scale, whichever is more; q is taken with 2^-18 of
- *   the row's largest value or exactly; out is rounded to bf16 (nearest even).
+ *   the head's largest p * v_scale, whichever is more; q is taken exactly or
+ *   with 2^-11 of its head's largest value at worst (2^-17 where the row's heads
+ *   are of one size); out is rounded to bf16 (nearest even).
  *   No workspace: the rows of small steps are split over thread-block clusters
  *   and joined in shared memory.
  *   Errors: K + W = 0 is SA_ERR_INVALID_ARG; SA_ERR_UNSUPPORTED if B * S_max

@@ -133,3 +133,30 @@ def test_keys_of_the_smallest_value_scale_weigh_as_much_as_any(sa, Hq, T, order)
         o, z, aw, rel = want(x, sb, torch.arange(int(x["nv"][r])), r, d ** -0.5)
         assert ((lse[r] - z).abs() <= rel + 2.0 ** -22 * z.abs()).all(), float((lse[r] - z).abs().max())
         assert ((out[r] - o).abs() <= 2.0 ** -8 * o.abs() + (2.0 ** -10 + rel) * aw).all()
+
+
+@pytest.mark.parametrize("Hq,d,T,paged_tiles", [(16, 128, 1, 1), (64, 128, 1, 9), (32, 128, 3, 4), (16, 64, 300, 3), (64, 128, 300, 5),
+                                                (33, 128, 320, 2)])
+def test_a_head_of_large_queries_leaves_the_others_their_precision(sa, Hq, d, T, paged_tiles):
+    """One head's queries are 2^20 times the others' (and one head is all zeros): the others' outputs and lse are as exact
+    as without it.  Rows in which heads lie 2^5 apart, or in which every head is large, go with them."""
+    n, sb = 128 * paged_tiles, 64
+    n = max(n, (T + 63) // 64 * 64)
+    x = sink_inputs(T, Hq, d, n, sb, 1.0, 1.0, 0, seed=70 + T)
+    q = x["q"].double()
+    q[..., 0] = 0
+    q[:, 1] *= 2.0 ** 20
+    q[:, 2] = 0
+    q[T // 2, 1] *= 2.0 ** -15
+    q[T - 1, 3:] *= 2.0 ** 20 if T > 1 else 1.0
+    x["q"] = q.bfloat16()
+    out, lse = run(sa, x, 1, T, 0, n, sb)
+    for r in sorted({0, T // 2, T - 1}):
+        keys = torch.arange(int(x["nv"][r]))
+        for h in [0, 2, 4, Hq - 1]:
+            if q[r, h].abs().max() > 100:
+                continue   # a head of large scores
+            alone = dict(x, q=x["q"][:, h:h + 1])   # its own slack, not the row's
+            o, z, aw, rel = want(alone, sb, keys, r, d ** -0.5)
+            assert ((lse[r, h:h + 1] - z).abs() <= rel + 2.0 ** -22 * z.abs()).all(), (r, h)
+            assert ((out[r, h:h + 1] - o).abs() <= 2.0 ** -8 * o.abs() + (2.0 ** -10 + rel) * aw).all(), (r, h)
