@@ -5,9 +5,10 @@
 //   x'_first  = x_first cos a_i - x_second sin a_i,   a_i = p * inv_freq[i]
 //   x'_second = x_second cos a_i + x_first sin a_i
 //
-// The angle p * inv_freq[i] is an exact fp64 product (a position below 2^31
-// times 24 bits); its turn count's fraction is taken in fp64 and only then
-// handed to fp32 sine and cosine, so that positions far out lose nothing.
+// The angle p * inv_freq[i] (a position below 2^31 times 24 bits: 55) is an fp64
+// product and what it rounds off, its turns likewise, with 1 / (2 pi) in two parts;
+// their fraction is taken in fp64 and only then handed to fp32 sine and cosine, so
+// that positions far out lose nothing.
 //
 // The step is bound by its bytes (the queries of all heads make nearly all of
 // them) at prompt lengths, and by one launch's latency for single tokens: 8192
@@ -54,8 +55,10 @@ __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 
 
 // cos and sin of p * f (see the head of the file)
 __device__ __forceinline__ float2 turn(int p, float f) {
-    const double t = (double)p * (double)f * 0.15915494309189535;
-    const float x = (float)(2.0 * (t - rint(t)));   // the angle in half turns, -1 .. 1
+    const double a = (double)p * (double)f, a_lo = fma((double)p, (double)f, -a);
+    const double turn = 0.15915494309189535, turn_lo = -9.839338337591243e-18;   // 1 / (2 pi)
+    const double t = a * turn, t_lo = fma(a, turn, -t) + fma(a, turn_lo, a_lo * turn);
+    const float x = (float)(2.0 * ((t - rint(t)) + t_lo));   // the angle in half turns, -1 .. 1
     float2 cs;
     sincospif(x, &cs.y, &cs.x);
     return cs;
