@@ -462,7 +462,11 @@ sa_status sa_cache_append(const sa_bf16 *q, int64_t ld_q, sa_bf16 *q_out,
  *   the step's last token are left as they are.
  *   The valid rows of a sequence must be consecutive rows with consecutive
  *   positions (padding only in front or behind): otherwise SA_DEV_ORDER, and
- *   nothing of that sequence is written but its q_out rows.  T is at most
+ *   nothing of that sequence is written but its q_out rows.  Likewise, and
+ *   unlike the 16-bit append, an n_valid out of range (SA_DEV_INDEX) leaves the
+ *   whole sequence unwritten but for the q_out of its other rows, since its run
+ *   of positions is not known; a page id outside of the pool leaves the step's
+ *   tokens of that page unwritten.  T is at most
  *   131072 (SA_ERR_UNSUPPORTED: append longer prompts in several calls). */
 sa_status sa_cache_append_q8(const sa_bf16 *q, int64_t ld_q, sa_bf16 *q_out,
                              const sa_bf16 *k, int64_t ld_k, const sa_bf16 *v,
