@@ -53,12 +53,17 @@ struct AppendParams {
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 
-// cos and sin of p * f (see the head of the file)
+// cos and sin of p * f (see the head of the file).  FAR: with what the products round off,
+// under 2^-31 of a turn below kNear.  (The registers for it spill with 16-bit caches: 2 x 2048
+// rows of 16 heads 14.1 us with, 12.8 without, so that a launch takes it by the cache's length.)
+constexpr int kNear = 1 << 24;
+template <bool FAR>
 __device__ __forceinline__ float2 turn(int p, float f) {
-    const double a = (double)p * (double)f, a_lo = fma((double)p, (double)f, -a);
     const double turn = 0.15915494309189535, turn_lo = -9.839338337591243e-18;   // 1 / (2 pi)
-    const double t = a * turn, t_lo = fma(a, turn, -t) + fma(a, turn_lo, a_lo * turn);
-    const float x = (float)(2.0 * ((t - rint(t)) + t_lo));   // the angle in half turns, -1 .. 1
+    const double a = (double)p * (double)f, t = a * turn;
+    double part = t - rint(t);
+    if (FAR) part += fma(a, turn, -t) + fma(a, turn_lo, fma((double)p, (double)f, -a) * turn);
+    const float x = (float)(2.0 * part);   // the angle in half turns, -1 .. 1
     float2 cs;
     sincospif(x, &cs.y, &cs.x);
     return cs;
@@ -125,7 +130,7 @@ __device__ __forceinline__ void rotate8(uint4 &a, uint4 &b, const float2 *cs) {
     }
 }
 
-template <bool INTER>
+template <bool INTER, bool FAR>
 __device__ __forceinline__ void append_rows(const AppendParams &P, int cta, float2 (*cs)[64], int64_t *slot, int *pos) {
     const AppendArgs &a = P.a;
     const int R = a.B * a.T, r0 = cta * P.rows, nr = min(P.rows, R - r0), half = a.rot_dim / 2, tid = threadIdx.x;
@@ -167,7 +172,7 @@ __device__ __forceinline__ void append_rows(const AppendParams &P, int cta, floa
     load2(tid);
     for (int i = tid; i < nr * half; i += kAThreads) {
         const int rl = i / half, f = i - rl * half, n = __ldg(a.n_valid + r0 + rl);
-        if (n > 0) cs[rl][f] = turn(n - 1, __ldg(a.inv_freq + f));
+        if (n > 0) cs[rl][f] = turn<FAR>(n - 1, __ldg(a.inv_freq + f));
     }
     if (tid >= kAThreads - 32 && tid - (kAThreads - 32) < nr) {   // (the angles rarely reach the last warp)
         const int rl = tid - (kAThreads - 32), r = r0 + rl, n = __ldg(a.n_valid + r);
@@ -232,7 +237,7 @@ __device__ __forceinline__ uint32_t finite_abs(float x) {   // bits of |x|, 0 fo
 }
 
 // One side of a page, or of a part of it: its new keys (rotated) or values.
-template <int D, bool INTER, bool KEYS>
+template <int D, bool INTER, bool KEYS, bool FAR>
 __device__ __forceinline__ void append_page(const AppendParams &P, int job, uint32_t *amax, float *scale, int *red, float *ratio) {
     constexpr int NV = D / 32, NW = kAThreads / 32, NT = kAPage / NW;   // values a lane, warps, tokens a warp
     const AppendArgs &a = P.a;
@@ -330,7 +335,7 @@ __device__ __forceinline__ void append_page(const AppendParams &P, int job, uint
         if (KEYS && INTER) {
 #pragma unroll
             for (int e = 0; e < NV / 2; ++e) {
-                const float2 c = rot ? turn(begin + tok, __ldg(a.inv_freq + d0 / 2 + e)) : make_float2(1.f, 0.f);
+                const float2 c = rot ? turn<FAR>(begin + tok, __ldg(a.inv_freq + d0 / 2 + e)) : make_float2(1.f, 0.f);
                 if (rot) {
                     x[i][2 * e] = y[2 * e] * c.x - y[2 * e + 1] * c.y;
                     x[i][2 * e + 1] = y[2 * e + 1] * c.x + y[2 * e] * c.y;
@@ -342,7 +347,7 @@ __device__ __forceinline__ void append_page(const AppendParams &P, int job, uint
             float2 mine[NV / 2];
 #pragma unroll
             for (int e = 0; e < NV / 2; ++e)
-                mine[e] = rot ? turn(begin + tok, __ldg(a.inv_freq + f0 + (upper ? NV / 2 : 0) + e)) : make_float2(1.f, 0.f);
+                mine[e] = rot ? turn<FAR>(begin + tok, __ldg(a.inv_freq + f0 + (upper ? NV / 2 : 0) + e)) : make_float2(1.f, 0.f);
 #pragma unroll
             for (int e = 0; e < NV / 2; ++e) {
                 const float2 other = make_float2(__shfl_sync(0xffffffffu, mine[e].x, partner),
@@ -406,8 +411,10 @@ __device__ __forceinline__ void append_page(const AppendParams &P, int job, uint
 
 // CTAs an SM: the row CTAs hold two units a thread in flight, and the more CTAs
 // share an SM the better they cover each other (8192 rows of 64 heads: 92 us with the
-// two that fit unbounded, 57 with four, 55 with five; six spill).
-template <int D, bool INTER, bool Q8>
+// two that fit unbounded, 57 with four, 55 with five, which spill 28 to 40 bytes with 128
+// dims; six spill 112 to 180).  With 16 bits eight spill 104 bytes with halves as pairs,
+// none with neighbours (2 x 2048 rows 12.8 us with eight, 14.3 with six).
+template <int D, bool INTER, bool Q8, bool FAR>
 __global__ void __launch_bounds__(kAThreads, Q8 ? 5 : 8) append_kernel(AppendParams P) {
     __shared__ float2 cs[kARowsMax][64];
     __shared__ int64_t slot[kARowsMax];
@@ -418,18 +425,23 @@ __global__ void __launch_bounds__(kAThreads, Q8 ? 5 : 8) append_kernel(AppendPar
             __shared__ uint32_t amax[kAPage];
             __shared__ float scale[kAPage], ratio;
             __shared__ int red[4];
-            if (job & 1) append_page<D, INTER, false>(P, job >> 1, amax, scale, red, &ratio);
-            else append_page<D, INTER, true>(P, job >> 1, amax, scale, red, &ratio);
+            if (job & 1) append_page<D, INTER, false, FAR>(P, job >> 1, amax, scale, red, &ratio);
+            else append_page<D, INTER, true, FAR>(P, job >> 1, amax, scale, red, &ratio);
             return;
         }
     }
-    append_rows<INTER>(P, (int)blockIdx.x - P.n_page_ctas, cs, slot, pos);
+    append_rows<INTER, FAR>(P, (int)blockIdx.x - P.n_page_ctas, cs, slot, pos);
 }
 
+template <int D, bool INTER, bool FAR>
+void launch_append_kernel(const AppendParams &P, unsigned grid, cudaStream_t st) {
+    if (P.a.q8) append_kernel<D, INTER, true, FAR><<<grid, kAThreads, 0, st>>>(P);
+    else append_kernel<D, INTER, false, FAR><<<grid, kAThreads, 0, st>>>(P);
+}
 template <int D, bool INTER>
 void launch_append_kernel(const AppendParams &P, unsigned grid, cudaStream_t st) {
-    if (P.a.q8) append_kernel<D, INTER, true><<<grid, kAThreads, 0, st>>>(P);
-    else append_kernel<D, INTER, false><<<grid, kAThreads, 0, st>>>(P);
+    if (P.a.S_max > kNear) launch_append_kernel<D, INTER, true>(P, grid, st);
+    else launch_append_kernel<D, INTER, false>(P, grid, st);
 }
 
 }  // namespace
