@@ -246,9 +246,6 @@ __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ float clamp_scale(float s) {   // into [2^-64, 2^64]; NaN -> 2^-64
-    return fminf(fmaxf(s, 5.421010862427522e-20f), 1.8446744073709552e19f);
-}
 // The address of this CTA's shared memory `local` in CTA `rank` of the cluster, and loads from such.
 __device__ __forceinline__ uint32_t in_cta(const void *local, uint32_t rank) {
     uint32_t remote;

@@ -104,9 +104,6 @@ __device__ __forceinline__ float scale_for(float amax) {
     const int e = min(64, max(-64, m <= 0.875f ? x - 9 : x - 8));
     return __int_as_float((e + 127) << 23);
 }
-__device__ __forceinline__ float clamp_scale(float s) {   // NaN -> 2^-64
-    return fminf(fmaxf(s, 5.421010862427522e-20f), 1.8446744073709552e19f);
-}
 
 // ------------------------------------------------------------------ rows
 // One chunk pair (halves) or chunk (interleaved) of 8 values, rotated.

@@ -43,6 +43,11 @@ sa_status launch_attn_q8(const AttnQ8Args &a, cudaStream_t st);
 // The same with `ctas` CTAs a row, whose waits give up after limit_ns, one for an MMA that never comes (d 128, Hq <= 16).
 sa_status launch_attn_q8_check(const AttnQ8Args &a, int ctas, int lost, unsigned long long limit_ns, cudaStream_t st);
 
+// A cached scale as a number in [2^-64, 2^64]; NaN -> 2^-64.
+__device__ __forceinline__ float clamp_scale(float s) {
+    return fminf(fmaxf(s, 5.421010862427522e-20f), 1.8446744073709552e19f);
+}
+
 // Cache rules shared by the append and the 8-bit attention: SA_OK when the
 // cache's sizes are within limits.
 inline sa_status check_cache_shape(const int32_t *page_table, int max_pages, int pool_pages, int page_size,
