@@ -53,14 +53,15 @@
 //
 // What bounds it.  Few rows: the launch and the chain row start -> lookups -> gather ->
 // S -> P -> P V -> join, of code that each CTA runs once: one row of 1152 keys 6.4 us, 8
-// rows of 2560 keys and 64 heads 10.5, 16 such paged rows 14.4.  While a CTA's MMAs run
-// neither the lookups nor reads of the scores get on, hence the order in the MMA warp.
-// Many rows: that same chain, two or three CTAs an SM deep, as many as V in fp16 leaves
-// room for.  2048 rows of 1152 keys and 16 heads 100 us (issue slots 56 percent, shared
-// memory 68), 4 x 1024 padded rows of up to 2560 keys and 64 heads 377 us (410 TFLOP/s).
-// V's codes in registers instead of a stage of their own in shared memory: 106 and 379;
-// both copies before the barrier of the tile: 107 and 393.  Every wait is bounded
-// (SA_DEV_TIMEOUT).
+// rows of 2560 keys and 64 heads 11.0, 16 such paged rows 15.3.  Alone on an SM a CTA's
+// tile takes 1.0 (16 heads) to 1.4 us (64): P V, V's widening, the barrier, P V; while its
+// MMAs run neither the lookups nor reads of the scores get on, hence the order in the MMA
+// warp.  Many rows: that same chain, two or three CTAs an SM deep, as many as V in fp16
+// leaves room for.  2048 rows of 1152 keys and 16 heads 104 us, of which the rows' starts and
+// ends are 23 (issue slots 56 percent); 4 x 1024 padded rows of up to 2560 keys and 64
+// heads 389 us (397 TFLOP/s), bound to 72 registers a thread.  V's codes in a stage of
+// their own in shared memory instead of registers took 6 and 0 percent longer, with both
+// copies before the barrier of the tile 7 and 4.  Every wait is bounded (SA_DEV_TIMEOUT).
 #include <math_constants.h>
 
 #include <algorithm>
@@ -1062,7 +1063,7 @@ __global__ void __launch_bounds__(Cfg<D, HQP>::kThreads, Cfg<D, HQP>::kPerSm) at
     if (CL) {
         // Join the parts of the heads rank * hpr ..: a warp a head, D / 32 dims a lane, so that a
         // load takes a whole row of one CTA's memory.  (16 paged rows of 2560 keys and 64 heads
-        // 15.1 us; with each lane of four taking every fourth part of 4 dims, so that a load went
+        // 15 us; with each lane of four taking every fourth part of 4 dims, so that a load went
         // to four CTAs, 16.1.)
         constexpr int V = D / 32, AT = 10;   // dims a lane, parts on their way at once
         const int hb = rank * P.hpr, nh = n_keys > 0 ? max(0, min(P.hpr, A.Hq - hb)) : 0;
@@ -1174,9 +1175,9 @@ sa_status launch_q8_rows(const AttnQ8Args &a, cudaStream_t st) {
     // CTAs a row.  In units of one tile's time in a cluster (1.0 us with 16 heads, 1.9
     // with 64), alone on an SM, a cluster takes 5.4 for its row's start and join and 1 a
     // tile, a single CTA 3.2 and 0.85; another CTA on the SM costs all of them 24 percent
-    // with up to 32 heads, 33 with 64 (fitted to rows of 4 to 40 tiles, 1 to 300 rows, where
-    // it is 1 percent off the best on average: 8 rows of 20 tiles and 64 heads 12.0 us with
-    // 10 CTAs a row, 36.7 with one, 15.8 with 16; 100 such rows 41.4 us with one, 43.4 with 4).
+    // with up to 32 heads, 33 with 64 (over rows of 2 to 40 tiles, 1 to 304 rows, it is 0.5
+    // percent off the best on average, 15 at worst: 8 rows of 20 tiles and 64 heads 10.5 us
+    // with 10 CTAs a row, 33.5 with one, 14.5 with 4; 112 such rows 34 with one, 40 with 4).
     p.G = 1;
     double best = 0;
     if (prepare_kernel<attn_q8_kernel<D, HQP, true>>(C::kSmem, true) != cudaSuccess) return SA_ERR_CUDA;
